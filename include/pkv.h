@@ -96,6 +96,9 @@ typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_FP8_E4M3 = 2, PKV_FP8_E5M2 = 3, PK
 #define PKV_DEVERR_SLOT 4      /* append slot >= num_blocks * block_size: row skipped */
 #define PKV_DEVERR_TIMEOUT 8   /* a bounded pipeline wait gave up (output incomplete) */
 #define PKV_DEVERR_PLAN 16     /* a shared-prefix plan entry out of range: that sequence's output is unspecified */
+#define PKV_DEVERR_ROWS 32     /* row_offsets not ascending within [0, num_tokens]: that sequence's rows skipped */
+#define PKV_DEVERR_POSITION 64 /* a position outside the cos / sin table: that token skipped */
+#define PKV_DEVERR_SELECTION 128 /* a selected block beyond its sequence: entry skipped */
 
 /*
  * Bytes of device workspace paged_attention_decode needs: a 256-byte header
@@ -355,6 +358,136 @@ PKV_API int reshape_and_cache(const void* k, const void* v, void* k_cache, void*
                       const int64_t* slot_mapping, int num_tokens, int num_kv_heads, int head_dim,
                       int block_size, int num_blocks, int in_dtype, int kv_dtype,
                       float k_scale, float v_scale, int32_t* device_error, void* stream);
+
+/*
+ * Norms of the queries and keys of each head, with the position rotation in the same pass. Every
+ * head's row x of head_dim elements becomes
+ *   y = x / sqrt(mean(x^2) + eps) * weight
+ * and then each of its rotary_dim / 2 pairs (a, b) becomes (a c - b s, b c + a s), c and s from row
+ * positions[t] of cos_sin; elements from rotary_dim on are not rotated. Computed in fp32, each
+ * output rounded once.
+ *
+ *   q_out, k_out   [num_tokens][num_heads or num_kv_heads][head_dim], dtype, contiguous. They may
+ *                  be q / k themselves (contiguous ones); no other overlap with an input.
+ *   q, k, v        rows of num_heads (num_kv_heads) * head_dim contiguous elements, consecutive
+ *                  tokens q_stride / k_stride / v_stride elements apart (a projection's output
+ *                  holding all three can be passed as it is). 16-byte aligned, as are the strides.
+ *   q_weight, k_weight  [head_dim] of dtype: one weight for every head of q, one for k
+ *   cos_sin        float [num_positions][rotary_dim], 16-byte aligned: the row's rotary_dim / 2
+ *                  cosines, then its sines
+ *   positions      int64 [num_tokens]; outside [0, num_positions): PKV_DEVERR_POSITION, nothing
+ *                  of that token is written
+ *   rotary_dim     0 .. head_dim, a multiple of 8
+ *   interleaved    0: pair i is elements (i, i + rotary_dim / 2); else elements (2i, 2i + 1)
+ *   dtype          PKV_F32 or PKV_BF16 (rows, weights and outputs)
+ *   device_error   optional int32 device word
+ * qk_norm_rope_and_cache also appends: the new K row, and the V row as it is, go to slot
+ * slot_mapping[t] of the caches, converted from fp32 as reshape_and_cache converts (8-bit caches
+ * with per-tensor scales); a negative slot appends nothing, and its q row is still written.
+ * Any num_heads, num_kv_heads >= 1. head_dim 64 or 128, block_size 8, 16 or 32.
+ */
+PKV_API int qk_norm_rope(void* q_out, void* k_out, const void* q, const void* k, const void* q_weight,
+                         const void* k_weight, float eps, const float* cos_sin, const int64_t* positions,
+                         int num_tokens, int num_heads, int num_kv_heads, int head_dim, int rotary_dim,
+                         int num_positions, int interleaved, int64_t q_stride, int64_t k_stride, int dtype,
+                         int32_t* device_error, void* stream);
+PKV_API int qk_norm_rope_and_cache(void* q_out, const void* q, const void* k, const void* v, const void* q_weight,
+                                   const void* k_weight, float eps, const float* cos_sin, const int64_t* positions,
+                                   void* k_cache, void* v_cache, const int64_t* slot_mapping, int num_tokens,
+                                   int num_heads, int num_kv_heads, int head_dim, int rotary_dim, int num_positions,
+                                   int block_size, int num_blocks, int interleaved, int64_t q_stride,
+                                   int64_t k_stride, int64_t v_stride, int in_dtype, int kv_dtype, float k_scale,
+                                   float v_scale, int32_t* device_error, void* stream);
+
+/*
+ * 8-bit caches with one scale for each block and KV head: k_block_scales / v_block_scales are
+ * device arrays float [num_blocks][num_kv_heads], and the value of a code is code * scale of its
+ * (block, KV head).
+ *
+ * The append takes its rows by sequence, since a block's scale depends on all that it holds:
+ *   row_offsets    int32 [num_seqs + 1], ascending: rows row_offsets[s] .. row_offsets[s + 1] - 1
+ *                  of k and v are sequence s's newest tokens (none is fine), at positions
+ *                  seq_lens[s] - n .. seq_lens[s] - 1 (seq_lens counts them). Rows behind the last
+ *                  sequence's are not read. Entries out of order or range: PKV_DEVERR_ROWS; more
+ *                  rows than tokens, or a length beyond the table: PKV_DEVERR_SEQ_LEN; such a
+ *                  sequence is skipped.
+ *   k, v           as in qk_norm_rope (k_stride, v_stride in elements), in_dtype F32 or BF16
+ * A block's scale becomes the smallest power of two 2^e, e in -50 .. 50, with
+ * max |x| <= qmax * 2^e (qmax 448 for E4M3, 57344 for E5M2, 127 for INT8) over the finite new rows
+ * of the block. If the block holds older tokens of the sequence (it had some before this call) the
+ * scale never becomes smaller than it was, and where it grows the older codes are re-encoded.
+ * Codes are the nearest ones of x / scale (ties to even), saturated; NaN gives a NaN code (INT8: 0).
+ * A block that another sequence reads too must not be appended to (copy it, with its scales, as
+ * for any append). kv_dtype FP8_E4M3, FP8_E5M2 or INT8; head_dim 64 or 128, block_size 8, 16 or 32.
+ *
+ * paged_attention_decode_block_scales is paged_attention_decode over such a cache. Any positive
+ * scales can be given, V scales within 2^-50 .. 2^50 (others are taken as the nearest of these).
+ * Shapes as the tensor-core kernel's 8-bit ones (bf16 q, head_dim 128, block_size 16 or 32).
+ */
+PKV_API int reshape_and_cache_block_scales(const void* k, const void* v, void* k_cache, void* v_cache,
+                                           float* k_block_scales, float* v_block_scales,
+                                           const int32_t* block_tables, const int32_t* seq_lens,
+                                           const int32_t* row_offsets, int num_tokens, int num_seqs,
+                                           int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                                           int num_blocks, int64_t k_stride, int64_t v_stride, int in_dtype,
+                                           int kv_dtype, int32_t* device_error, void* stream);
+PKV_API int paged_attention_decode_block_scales(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                                const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
+                                                int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                                float scale, int max_blocks_per_seq, int num_blocks, int q_dtype,
+                                                int kv_dtype, const float* k_block_scales,
+                                                const float* v_block_scales, int num_partitions, void* workspace,
+                                                size_t workspace_bytes, void* stream);
+
+/*
+ * Decode attention over a part of the blocks, chosen for each sequence and KV head.
+ *
+ * update_key_bounds keeps, for every (block, KV head), the largest and the smallest value of each
+ * key dimension over the tokens of the block:
+ *   key_bounds     bf16 [num_blocks][num_kv_heads][2][head_dim]: maxima, then minima
+ * for every block that holds one of the num_tokens newest tokens (row_offsets, seq_lens as in
+ * reshape_and_cache_block_scales; the keys are taken from the cache, after the append). Exact for
+ * bf16 caches; 8-bit caches give the nearest bf16 of code * scale (k_block_scales, or null and
+ * k_scale). kv_dtype BF16, FP8_E4M3, FP8_E5M2 or INT8.
+ *
+ * select_blocks writes, for every sequence s and KV head h, num_selected logical blocks in
+ * ascending order to selected[s][h][:] (int32 [num_seqs][num_kv_heads][num_selected]): all of
+ * them, and -1 behind, if the sequence has no more; else its first num_sink_blocks, its last
+ * num_recent_blocks, and of the others those with the highest
+ *   score(j) = max over the query heads g of h of sum_d max(q[s][g][d] * max_d, q[s][g][d] * min_d),
+ * an upper bound of the products of the block's keys with these queries. Ties go to the lowest
+ * index; sums that fp32 cannot tell apart are formed again in fp64. A block whose score is not
+ * finite ranks first, one with a bad block id (PKV_DEVERR_BLOCK_ID) last. q is bf16. The
+ * workspace (pkv_select_workspace_size bytes) starts zeroed (pkv_workspace_init) and holds the
+ * error word; one can serve calls of any sizes it is large enough for, but calls that share one
+ * must not overlap on the GPU. num_seqs * num_kv_heads <= 2^18; groups as everywhere.
+ *
+ * paged_attention_decode_sparse attends, for KV head h of sequence s, the tokens of the listed
+ * blocks only. Of a list the first min(num_selected, ceil(seq_lens[s] / block_size)) entries are
+ * used; negative ones are empty, ones beyond the sequence set PKV_DEVERR_SELECTION and are empty
+ * too; a block listed twice counts twice; a list without a token gives zero rows. Order does not
+ * matter but for rounding. Scales: k_block_scales and v_block_scales (both, or null and k_scale,
+ * v_scale) for 8-bit caches. Shapes as the tensor-core kernel's (bf16 q; bf16 caches with head_dim
+ * 64 or 128, 8-bit ones with 128; block_size 16 or 32). Workspace as paged_attention_decode's.
+ */
+PKV_API int update_key_bounds(void* key_bounds, const void* k_cache, const int32_t* block_tables,
+                              const int32_t* seq_lens, const int32_t* row_offsets, int num_tokens, int num_seqs,
+                              int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
+                              int kv_dtype, float k_scale, const float* k_block_scales, int32_t* device_error,
+                              void* stream);
+PKV_API size_t pkv_select_workspace_size(int num_seqs, int num_kv_heads, int max_blocks_per_seq);
+PKV_API int select_blocks(int32_t* selected, const void* q, const void* key_bounds, const int32_t* block_tables,
+                          const int32_t* seq_lens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                          int block_size, int max_blocks_per_seq, int num_blocks, int num_selected,
+                          int num_sink_blocks, int num_recent_blocks, void* workspace, size_t workspace_bytes,
+                          void* stream);
+PKV_API int paged_attention_decode_sparse(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                          const int32_t* block_tables, const int32_t* seq_lens,
+                                          const int32_t* selected, int num_seqs, int num_heads, int num_kv_heads,
+                                          int head_dim, int block_size, float scale, int max_blocks_per_seq,
+                                          int num_blocks, int num_selected, int q_dtype, int kv_dtype, float k_scale,
+                                          float v_scale, const float* k_block_scales, const float* v_block_scales,
+                                          int num_partitions, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Copy the workspace's device error word to *host_error (synchronising on

@@ -13,6 +13,12 @@ Entry points (same names as the C ABI):
 * ``paged_attention_decode(out, q, k_cache, v_cache, block_tables, seq_lens,
   scale, ...)`` — single-query grouped attention for every sequence, reading
   K/V block by block through the block table.
+* ``qk_norm_rope`` / ``qk_norm_rope_and_cache`` — per-head RMS norm of queries and
+  keys with the position rotation, and the append in the same pass.
+* ``reshape_and_cache_block_scales`` / ``paged_attention_decode_block_scales`` — an
+  8-bit cache with one scale for each block and KV head.
+* ``update_key_bounds``, ``select_blocks``, ``paged_attention_decode_sparse`` — decode
+  attention over the blocks a cheap score selects for each query.
 """
 from __future__ import annotations
 
@@ -26,6 +32,7 @@ LIB_PATH = os.path.join(HERE, "libpagedkv.so")
 
 F32, BF16, FP8_E4M3, FP8_E5M2, INT8 = 0, 1, 2, 3, 4
 DEVERR_BLOCK_ID, DEVERR_SEQ_LEN, DEVERR_SLOT, DEVERR_TIMEOUT, DEVERR_PLAN = 1, 2, 4, 8, 16
+DEVERR_ROWS, DEVERR_POSITION, DEVERR_SELECTION = 32, 64, 128
 
 # uint8 caches hold E4M3 codes; E5M2 caches are passed as torch.float8_e5m2 tensors
 _TORCH_DTYPE = {torch.float32: F32, torch.bfloat16: BF16, torch.uint8: FP8_E4M3, torch.float8_e4m3fn: FP8_E4M3,
@@ -88,6 +95,27 @@ def load_library():
                                                     i32, f32, f32, P, P, P, P, P, i32, i32, i32, P, sz, P, P, P,
                                                     i32, P]
     lib.paged_decode_step_shared_prefix.restype = i32
+    i64 = ctypes.c_int64
+    lib.qk_norm_rope.argtypes = [P, P, P, P, P, P, f32, P, P, i32, i32, i32, i32, i32, i32, i32, i64, i64, i32, P, P]
+    lib.qk_norm_rope.restype = i32
+    lib.qk_norm_rope_and_cache.argtypes = [P, P, P, P, P, P, f32, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32,
+                                           i32, i32, i64, i64, i64, i32, i32, f32, f32, P, P]
+    lib.qk_norm_rope_and_cache.restype = i32
+    lib.reshape_and_cache_block_scales.argtypes = [P, P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, i64,
+                                                   i64, i32, i32, P, P]
+    lib.reshape_and_cache_block_scales.restype = i32
+    lib.paged_attention_decode_block_scales.argtypes = [P, P, P, P, P, P, i32, i32, i32, i32, i32, f32, i32, i32, i32,
+                                                        i32, P, P, i32, P, sz, P]
+    lib.paged_attention_decode_block_scales.restype = i32
+    lib.update_key_bounds.argtypes = [P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, i32, f32, P, P, P]
+    lib.update_key_bounds.restype = i32
+    lib.pkv_select_workspace_size.argtypes = [i32, i32, i32]
+    lib.pkv_select_workspace_size.restype = sz
+    lib.select_blocks.argtypes = [P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, i32, i32, i32, P, sz, P]
+    lib.select_blocks.restype = i32
+    lib.paged_attention_decode_sparse.argtypes = [P, P, P, P, P, P, P, i32, i32, i32, i32, i32, f32, i32, i32, i32,
+                                                  i32, i32, f32, f32, P, P, i32, P, sz, P]
+    lib.paged_attention_decode_sparse.restype = i32
     lib.pkv_validate_tables.argtypes = [P, P, i32, i32, i32, i32, P, ctypes.POINTER(ctypes.c_int32),
                                         ctypes.POINTER(ctypes.c_int32)]
     lib.pkv_validate_tables.restype = i32
@@ -465,6 +493,283 @@ def validate_tables(block_tables, seq_lens, block_size: int, num_blocks: int, sl
     return int(bits.value), int(first.value)
 
 
+def _rows(name, t, dev, heads=None, dim=None, dtype=None):
+    """(device pointer, tokens, heads, head_dim, token stride) of rows [tokens, heads, head_dim] whose
+    heads are contiguous; tokens may lie further apart (a view of a projection's output)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [num_tokens, heads, head_dim]")
+    T, H, D = t.shape
+    if (heads is not None and H != heads) or (dim is not None and D != dim):
+        raise ValueError(f"{name} has another number of heads or another head_dim")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.device.index != dev:
+        raise ValueError(f"{name} is on {t.device}, the current CUDA device is cuda:{dev}")
+    if T > 0 and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if T > 1 and t.stride(0) < H * D:
+        raise ValueError(f"{name}: tokens must not share elements")
+    return ctypes.c_void_p(t.data_ptr()), T, H, D, (t.stride(0) if T > 1 else H * D)
+
+
+def _norm_rope_args(q_out, q, k, q_weight, k_weight, cos_sin, positions, dev):
+    """Checked pieces that qk_norm_rope and qk_norm_rope_and_cache share."""
+    qp, T, Hq, D, qs = _rows("q", q, dev)
+    kp, Tk, Hkv, _, ks = _rows("k", k, dev, dim=D, dtype=q.dtype)
+    if Tk != T or tuple(q_out.shape) != (T, Hq, D):
+        raise ValueError("shape mismatch between q, k and q_out")
+    if q_out.dtype != q.dtype or q_weight.dtype != q.dtype or k_weight.dtype != q.dtype:
+        raise TypeError("q_out and the weights must have q's dtype")
+    if q_weight.shape != (D,) or k_weight.shape != (D,):
+        raise ValueError("the weights must be [head_dim]")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+        raise TypeError("cos_sin must be float32 [num_positions, rotary_dim]")
+    if positions.dtype != torch.int64 or positions.shape != (T,):
+        raise TypeError("positions must be int64 [num_tokens]")
+    return qp, kp, T, Hq, Hkv, D, qs, ks
+
+
+def qk_norm_rope(q_out, k_out, q, k, q_weight, k_weight, eps, cos_sin, positions, interleaved=False,
+                 device_error=None, stream=None) -> None:
+    """q_out, k_out = rotate(rms_norm(q) * q_weight), rotate(rms_norm(k) * k_weight), head by head.
+
+    q [num_tokens, num_heads, head_dim], k [num_tokens, num_kv_heads, head_dim] (float32 or bfloat16;
+    views of a larger projection output are fine); q_out, k_out contiguous, or q and k themselves;
+    weights [head_dim]; cos_sin float32 [num_positions, rotary_dim] (cosines, then sines);
+    positions int64 [num_tokens]."""
+    dev = _launch_device("q", q)
+    qp, kp, T, Hq, Hkv, D, qs, ks = _norm_rope_args(q_out, q, k, q_weight, k_weight, cos_sin, positions, dev)
+    if tuple(k_out.shape) != (T, Hkv, D) or k_out.dtype != q.dtype:
+        raise ValueError("k_out must match k")
+    err = ctypes.c_void_p(None) if device_error is None else _cuda("device_error", device_error, dev)
+    st = load_library().qk_norm_rope(
+        _cuda("q_out", q_out, dev), _cuda("k_out", k_out, dev), qp, kp, _cuda("q_weight", q_weight, dev),
+        _cuda("k_weight", k_weight, dev), float(eps), _cuda("cos_sin", cos_sin, dev),
+        _cuda("positions", positions, dev), T, Hq, Hkv, D, cos_sin.shape[1], cos_sin.shape[0], int(bool(interleaved)),
+        qs, ks, _dtype_code(q), err, _stream_handle(stream))
+    _check("qk_norm_rope", st)
+
+
+def qk_norm_rope_and_cache(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, positions, k_cache, v_cache,
+                           slot_mapping, interleaved=False, k_scale=1.0, v_scale=1.0, device_error=None,
+                           stream=None) -> None:
+    """qk_norm_rope with the append of reshape_and_cache in the same pass: the new keys and the rows
+    of v go to slot slot_mapping[t] of the caches (a negative slot appends nothing)."""
+    dev = _launch_device("q", q)
+    qp, kp, T, Hq, Hkv, D, qs, ks = _norm_rope_args(q_out, q, k, q_weight, k_weight, cos_sin, positions, dev)
+    vp, Tv, _, _, vs = _rows("v", v, dev, heads=Hkv, dim=D, dtype=q.dtype)
+    NB, Hkv2, BS, D2 = k_cache.shape
+    if Tv != T or (Hkv2, D2) != (Hkv, D) or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("shape mismatch between rows and caches")
+    if v_cache.dtype != k_cache.dtype:
+        raise TypeError("v_cache must have k_cache's dtype")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
+        raise TypeError("slot_mapping must be int64 [num_tokens]")
+    err = ctypes.c_void_p(None) if device_error is None else _cuda("device_error", device_error, dev)
+    st = load_library().qk_norm_rope_and_cache(
+        _cuda("q_out", q_out, dev), qp, kp, vp, _cuda("q_weight", q_weight, dev), _cuda("k_weight", k_weight, dev),
+        float(eps), _cuda("cos_sin", cos_sin, dev), _cuda("positions", positions, dev), _cuda("k_cache", k_cache, dev),
+        _cuda("v_cache", v_cache, dev), _cuda("slot_mapping", slot_mapping, dev), T, Hq, Hkv, D, cos_sin.shape[1],
+        cos_sin.shape[0], BS, NB, int(bool(interleaved)), qs, ks, vs, _dtype_code(q), _dtype_code(k_cache),
+        float(k_scale), float(v_scale), err, _stream_handle(stream))
+    _check("qk_norm_rope_and_cache", st)
+
+
+def _tables(block_tables, seq_lens, dev):
+    """Checked (block_tables pointer, seq_lens pointer, num_seqs, max_blocks)."""
+    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+        raise TypeError("block_tables and seq_lens must be int32")
+    if block_tables.dim() != 2 or seq_lens.shape != (block_tables.shape[0],):
+        raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
+    return (_cuda("block_tables", block_tables, dev), _cuda("seq_lens", seq_lens, dev), block_tables.shape[0],
+            block_tables.shape[1])
+
+
+def _block_scales(name, t, cache, dev):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or tuple(t.shape) != tuple(cache.shape[:2]):
+        raise TypeError(f"{name} must be a float32 tensor [num_blocks, num_kv_heads]")
+    return _cuda(name, t, dev)
+
+
+def _row_offsets(t, S, dev):
+    if t.dtype != torch.int32 or t.shape != (S + 1,):
+        raise TypeError("row_offsets must be int32 [num_seqs + 1]")
+    return _cuda("row_offsets", t, dev)
+
+
+def reshape_and_cache_block_scales(k, v, k_cache, v_cache, k_block_scales, v_block_scales, block_tables, seq_lens,
+                                   row_offsets, device_error=None, stream=None) -> None:
+    """Append rows to an 8-bit cache with one power-of-two scale for each (block, KV head).
+
+    k, v [num_tokens, num_kv_heads, head_dim]: rows row_offsets[s] .. row_offsets[s + 1] - 1 are the
+    newest tokens of sequence s, which has seq_lens[s] tokens with them. The scales (float32
+    [num_blocks, num_kv_heads]) of the blocks they fall into are set, or grow (and the block's older
+    codes with them) where the block already holds tokens of the sequence."""
+    dev = _launch_device("k", k)
+    kp, T, Hkv, D, ks = _rows("k", k, dev)
+    vp, Tv, _, _, vs = _rows("v", v, dev, heads=Hkv, dim=D, dtype=k.dtype)
+    NB, Hkv2, BS, D2 = k_cache.shape
+    if Tv != T or (Hkv2, D2) != (Hkv, D) or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("shape mismatch between rows and caches")
+    if v_cache.dtype != k_cache.dtype:
+        raise TypeError("v_cache must have k_cache's dtype")
+    bt, sl, S, MB = _tables(block_tables, seq_lens, dev)
+    err = ctypes.c_void_p(None) if device_error is None else _cuda("device_error", device_error, dev)
+    st = load_library().reshape_and_cache_block_scales(
+        kp, vp, _cuda("k_cache", k_cache, dev), _cuda("v_cache", v_cache, dev),
+        _block_scales("k_block_scales", k_block_scales, k_cache, dev),
+        _block_scales("v_block_scales", v_block_scales, k_cache, dev), bt, sl, _row_offsets(row_offsets, S, dev), T, S,
+        Hkv, D, BS, MB, NB, ks, vs, _dtype_code(k), _dtype_code(k_cache), err, _stream_handle(stream))
+    _check("reshape_and_cache_block_scales", st)
+
+
+def _decode_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, dev):
+    S, Hq, D = q.shape
+    NB, Hkv, BS, D2 = k_cache.shape
+    if D2 != D or tuple(v_cache.shape) != tuple(k_cache.shape) or tuple(out.shape) != tuple(q.shape):
+        raise ValueError("shape mismatch between q/out and the caches")
+    if out.dtype != q.dtype or v_cache.dtype != k_cache.dtype:
+        raise TypeError("out must match q's dtype and v_cache k_cache's")
+    bt, sl, S2, MB = _tables(block_tables, seq_lens, dev)
+    if S2 != S:
+        raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
+    return S, Hq, D, NB, Hkv, BS, bt, sl, MB
+
+
+def paged_attention_decode_block_scales(out, q, k_cache, v_cache, block_tables, seq_lens, scale, k_block_scales,
+                                        v_block_scales, num_partitions=0, workspace=None, stream=None) -> None:
+    """paged_attention_decode over an 8-bit cache with one scale for each (block, KV head):
+    k_block_scales, v_block_scales float32 [num_blocks, num_kv_heads], positive."""
+    dev = _launch_device("q", q)
+    S, Hq, D, NB, Hkv, BS, bt, sl, MB = _decode_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, dev)
+    if workspace is None:
+        workspace = _op_workspace("decode", workspace_size(S, Hq, Hkv, D, num_partitions), 256, dev, stream)
+    st = load_library().paged_attention_decode_block_scales(
+        _cuda("out", out, dev), _cuda("q", q, dev), _cuda("k_cache", k_cache, dev), _cuda("v_cache", v_cache, dev),
+        bt, sl, S, Hq, Hkv, D, BS, float(scale), MB, NB, _dtype_code(q), _dtype_code(k_cache),
+        _block_scales("k_block_scales", k_block_scales, k_cache, dev),
+        _block_scales("v_block_scales", v_block_scales, k_cache, dev), int(num_partitions),
+        _cuda("workspace", workspace, dev), workspace.numel(), _stream_handle(stream))
+    _check("paged_attention_decode_block_scales", st)
+
+
+def update_key_bounds(key_bounds, k_cache, block_tables, seq_lens, row_offsets, num_tokens, k_scale=1.0,
+                      k_block_scales=None, device_error=None, stream=None) -> None:
+    """Refresh key_bounds (bfloat16 [num_blocks, num_kv_heads, 2, head_dim]: maxima, minima over a
+    block's keys) for the blocks that hold the num_tokens newest tokens of a batch, after their
+    append; row_offsets as in reshape_and_cache_block_scales (int32 [num_seqs + 1])."""
+    dev = _launch_device("k_cache", k_cache)
+    NB, Hkv, BS, D = k_cache.shape
+    if key_bounds.dtype != torch.bfloat16 or tuple(key_bounds.shape) != (NB, Hkv, 2, D):
+        raise TypeError("key_bounds must be bfloat16 [num_blocks, num_kv_heads, 2, head_dim]")
+    bt, sl, S, MB = _tables(block_tables, seq_lens, dev)
+    scales = ctypes.c_void_p(None) if k_block_scales is None else \
+        _block_scales("k_block_scales", k_block_scales, k_cache, dev)
+    err = ctypes.c_void_p(None) if device_error is None else _cuda("device_error", device_error, dev)
+    st = load_library().update_key_bounds(
+        _cuda("key_bounds", key_bounds, dev), _cuda("k_cache", k_cache, dev), bt, sl, _row_offsets(row_offsets, S, dev),
+        int(num_tokens), S, Hkv, D, BS, MB, NB, _dtype_code(k_cache), float(k_scale), scales, err,
+        _stream_handle(stream))
+    _check("update_key_bounds", st)
+
+
+def select_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq) -> int:
+    n = load_library().pkv_select_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq)
+    if n == 0:
+        raise PkvError("pkv_select_workspace_size", 2)
+    return int(n)
+
+
+def new_select_workspace(num_seqs, num_kv_heads, max_blocks_per_seq, device=None) -> torch.Tensor:
+    """A zeroed workspace for select_blocks."""
+    n = select_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq)
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def select_blocks(selected, q, key_bounds, block_tables, seq_lens, block_size, num_sink_blocks=1,
+                  num_recent_blocks=1, workspace=None, stream=None) -> None:
+    """selected[s, h] (int32 [num_seqs, num_kv_heads, num_selected]) = the logical blocks KV head h's
+    queries may need most, ascending, -1 behind where the sequence has fewer: the first
+    num_sink_blocks, the last num_recent_blocks and the highest scores of the rest, a block's score
+    being the bound that key_bounds sets to its keys' products with the group's queries.
+    q bfloat16 [num_seqs, num_heads, head_dim]."""
+    dev = _launch_device("q", q)
+    S, Hq, D = q.shape
+    NB, Hkv, two, D2 = key_bounds.shape
+    if q.dtype != torch.bfloat16 or key_bounds.dtype != torch.bfloat16:
+        raise TypeError("q and key_bounds must be bfloat16")
+    if two != 2 or D2 != D:
+        raise ValueError("key_bounds must be [num_blocks, num_kv_heads, 2, head_dim]")
+    if selected.dtype != torch.int32 or selected.dim() != 3 or tuple(selected.shape[:2]) != (S, Hkv):
+        raise TypeError("selected must be int32 [num_seqs, num_kv_heads, num_selected]")
+    bt, sl, S2, MB = _tables(block_tables, seq_lens, dev)
+    if S2 != S:
+        raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
+    if workspace is None:
+        workspace = _op_workspace("select", select_workspace_size(S, Hkv, max(1, MB)), 256 + (4 << 18), dev, stream)
+    st = load_library().select_blocks(
+        _cuda("selected", selected, dev), _cuda("q", q, dev), _cuda("key_bounds", key_bounds, dev), bt, sl, S, Hq, Hkv,
+        D, int(block_size), MB, NB, selected.shape[2], int(num_sink_blocks), int(num_recent_blocks),
+        _cuda("workspace", workspace, dev), workspace.numel(), _stream_handle(stream))
+    _check("select_blocks", st)
+
+
+def paged_attention_decode_sparse(out, q, k_cache, v_cache, block_tables, seq_lens, selected, scale, k_scale=1.0,
+                                  v_scale=1.0, k_block_scales=None, v_block_scales=None, num_partitions=0,
+                                  workspace=None, stream=None) -> None:
+    """paged_attention_decode over the tokens of the listed blocks only: selected int32 [num_seqs,
+    num_kv_heads, num_selected] (select_blocks' output), negative entries empty. 8-bit caches take
+    per-tensor scales or both block scales."""
+    dev = _launch_device("q", q)
+    S, Hq, D, NB, Hkv, BS, bt, sl, MB = _decode_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, dev)
+    if selected.dtype != torch.int32 or selected.dim() != 3 or tuple(selected.shape[:2]) != (S, Hkv):
+        raise TypeError("selected must be int32 [num_seqs, num_kv_heads, num_selected]")
+    if (k_block_scales is None) != (v_block_scales is None):
+        raise ValueError("give both block scales or none")
+    ks = vs = ctypes.c_void_p(None)
+    if k_block_scales is not None:
+        ks = _block_scales("k_block_scales", k_block_scales, k_cache, dev)
+        vs = _block_scales("v_block_scales", v_block_scales, k_cache, dev)
+    if workspace is None:
+        workspace = _op_workspace("decode", workspace_size(S, Hq, Hkv, D, num_partitions), 256, dev, stream)
+    st = load_library().paged_attention_decode_sparse(
+        _cuda("out", out, dev), _cuda("q", q, dev), _cuda("k_cache", k_cache, dev), _cuda("v_cache", v_cache, dev),
+        bt, sl, _cuda("selected", selected, dev), S, Hq, Hkv, D, BS, float(scale), MB, NB, selected.shape[2],
+        _dtype_code(q), _dtype_code(k_cache), float(k_scale), float(v_scale), ks, vs, int(num_partitions),
+        _cuda("workspace", workspace, dev), workspace.numel(), _stream_handle(stream))
+    _check("paged_attention_decode_sparse", st)
+
+
+_op_ws: dict = {}
+
+
+def _op_workspace(kind, n, zeroed, dev, stream):
+    """A workspace of at least n bytes, its first `zeroed` ones cleared, kept per (kind, device,
+    stream), so that calls on different streams never share one. It is allocated and cleared on the
+    stream that uses it. While that stream is being captured every call gets its own, from the
+    graph's memory and cleared inside the graph: two graphs, or a graph and later eager calls, then
+    never meet in one."""
+    handle = _stream_handle(stream)
+    current = torch.cuda.current_stream()
+    capturing = torch.cuda.is_current_stream_capturing()
+    if capturing and handle.value != ctypes.c_void_p(current.cuda_stream).value:
+        raise ValueError("pass a workspace to capture on another stream than the current one")
+    key = (kind, dev, handle.value)
+    ws = None if capturing else _op_ws.get(key)
+    if ws is None or ws.numel() < n:
+        on = current if handle.value == ctypes.c_void_p(current.cuda_stream).value else \
+            torch.cuda.ExternalStream(handle.value or 0, device=dev)
+        with torch.cuda.stream(on):
+            ws = torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", dev))
+        _check("pkv_workspace_init",
+               load_library().pkv_workspace_init(_cuda("workspace", ws), min(n, zeroed), handle))
+        if not capturing:
+            _op_ws[key] = ws
+    return ws
+
+
 _ws_cache: dict = {}
 
 
@@ -490,5 +795,8 @@ __all__ = [
     "read_device_error", "default_partitions", "status_string", "load_library", "PkvError",
     "paged_attention_decode_shared_prefix", "paged_decode_step_shared_prefix", "DevicePrefixPlan",
     "shared_prefix_workspace_size", "new_shared_prefix_workspace", "validate_tables",
+    "qk_norm_rope", "qk_norm_rope_and_cache", "reshape_and_cache_block_scales", "paged_attention_decode_block_scales",
+    "update_key_bounds", "select_blocks", "select_workspace_size", "new_select_workspace",
+    "paged_attention_decode_sparse",
     "F32", "BF16", "FP8_E4M3", "FP8_E5M2", "INT8",
 ]

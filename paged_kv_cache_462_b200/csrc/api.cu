@@ -392,9 +392,125 @@ int decode_impl(void* out, const void* q, const void* k_cache, const void* v_cac
                            static_cast<cudaStream_t>(stream), nullptr);
 }
 
+// A launch on `stream` is being recorded into a graph. A replay repeats the recorded parameters,
+// the call's epoch among them, so that a chunk's stamp of the replay before would pass for its own:
+// a recorded merge waits for the whole decode grid instead of the stamps.
+bool recorded(cudaStream_t stream)
+{
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &status) != cudaSuccess) {
+        (void)cudaGetLastError();   // the legacy stream while another one captures: not recorded
+        return false;
+    }
+    return status != cudaStreamCaptureStatusNone;
+}
+
+// The decodes whose producer resolves every KV head for itself: over selected blocks, over a cache
+// with block scales, or both. Tensor-core shapes only.
+int heads_impl(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+               const int32_t* seq_lens, int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+               float scale, int max_blocks_per_seq, int num_blocks, int q_dtype, int kv_dtype, float k_scale,
+               float v_scale, const int32_t* selected, int num_selected, const float* k_block_scales,
+               const float* v_block_scales, int num_partitions, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 || num_partitions < 0)
+        return PKV_ERR_SHAPE;
+    const int group = num_heads / num_kv_heads;
+    if (q_dtype != PKV_BF16 || (kv_dtype != PKV_BF16 && !is_fp8(kv_dtype)))
+        return PKV_ERR_DTYPE;
+    if (!group_supported(group) || !mma_supported(kv_dtype, head_dim, block_size, group, num_kv_heads))
+        return PKV_ERR_SHAPE;
+    const bool scaled = k_block_scales || v_block_scales;
+    if (scaled && !is_fp8(kv_dtype))
+        return PKV_ERR_DTYPE;
+    if (scaled && (!k_block_scales || !v_block_scales))
+        return PKV_ERR_NULL;
+    if (!scaled && is_fp8(kv_dtype) && !(k_scale > 0.0f && v_scale > 0.0f))
+        return PKV_ERR_SHAPE;
+    if (num_seqs == 0)
+        return PKV_OK;
+    int runs = num_partitions;
+    const int HG = mma_head_group(kv_dtype, head_dim, block_size, num_kv_heads);
+    MmaOp op{};
+    if (runs == 0 && num_seqs <= kMaxSeqs) {
+        const int dev = current_device();
+        const int sms = dev >= 0 ? sm_count(dev) : 0;
+        if (sms <= 0)
+            return PKV_ERR_DEVICE;
+        DecodeParams probe;
+        std::memset(&probe, 0, sizeof probe);
+        probe.num_seqs = num_seqs;
+        int occ = 0;
+        op.kind = MmaOp::kPerHeadOccupancy;
+        op.p = &probe;
+        op.occ = &occ;
+        const int st = decode_mma_op(kv_dtype, head_dim, block_size, group, HG, op);
+        if (st != PKV_OK)
+            return st;
+        if (occ < 1)
+            return PKV_ERR_SHAPE;
+        runs = sms * (occ > kMaxRunsPerSM ? kMaxRunsPerSM : occ);
+    }
+    DecodeParams p;
+    const int st = decode_prepare(out, q, k_cache, v_cache, block_tables, seq_lens, num_seqs, num_heads, num_kv_heads,
+                                  head_dim, block_size, scale, max_blocks_per_seq, num_blocks, q_dtype, kv_dtype,
+                                  scaled ? 1.0f : k_scale, scaled ? 1.0f : v_scale, runs, workspace, workspace_bytes,
+                                  nullptr, -1, 1, nullptr, nullptr, &p, &runs);
+    if (st != PKV_OK || runs == 0)
+        return st;
+    p.selected = selected;
+    p.sel_width = num_selected;
+    p.k_block_scales = k_block_scales;
+    p.v_block_scales = v_block_scales;
+    if (recorded(static_cast<cudaStream_t>(stream)))
+        p.chunk_done = nullptr;
+    op = MmaOp{};
+    op.kind = MmaOp::kLaunchPerHead;
+    op.p = &p;
+    op.nruns = runs;
+    op.stream = static_cast<cudaStream_t>(stream);
+    return decode_mma_op(kv_dtype, head_dim, block_size, group, HG, op);
+}
+
 }  // namespace
 
 extern "C" {
+
+int paged_attention_decode_block_scales(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                        const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
+                                        int num_heads, int num_kv_heads, int head_dim, int block_size, float scale,
+                                        int max_blocks_per_seq, int num_blocks, int q_dtype, int kv_dtype,
+                                        const float* k_block_scales, const float* v_block_scales, int num_partitions,
+                                        void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (!is_fp8(kv_dtype))
+        return PKV_ERR_DTYPE;
+    if (num_seqs > 0 && (!k_block_scales || !v_block_scales))
+        return PKV_ERR_NULL;
+    return heads_impl(out, q, k_cache, v_cache, block_tables, seq_lens, num_seqs, num_heads, num_kv_heads, head_dim,
+                      block_size, scale, max_blocks_per_seq, num_blocks, q_dtype, kv_dtype, 1.0f, 1.0f, nullptr, 0,
+                      k_block_scales, v_block_scales, num_partitions, workspace, workspace_bytes, stream);
+}
+
+int paged_attention_decode_sparse(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_tables, const int32_t* seq_lens, const int32_t* selected,
+                                  int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                  float scale, int max_blocks_per_seq, int num_blocks, int num_selected, int q_dtype,
+                                  int kv_dtype, float k_scale, float v_scale, const float* k_block_scales,
+                                  const float* v_block_scales, int num_partitions, void* workspace,
+                                  size_t workspace_bytes, void* stream)
+{
+    if (num_selected < 1 || num_seqs < 0 || num_kv_heads <= 0 ||
+        (long long)num_seqs * num_kv_heads * num_selected >= (1ll << 31) ||
+        (block_size > 0 && (long long)num_selected * block_size >= (1ll << 31)))
+        return PKV_ERR_SHAPE;
+    if (num_seqs > 0 && !selected)
+        return PKV_ERR_NULL;
+    return heads_impl(out, q, k_cache, v_cache, block_tables, seq_lens, num_seqs, num_heads, num_kv_heads, head_dim,
+                      block_size, scale, max_blocks_per_seq, num_blocks, q_dtype, kv_dtype, k_scale, v_scale, selected,
+                      num_selected, k_block_scales, v_block_scales, num_partitions, workspace, workspace_bytes,
+                      stream);
+}
 
 int paged_attention_decode(void* out, const void* q, const void* k_cache, const void* v_cache,
                            const int32_t* block_tables, const int32_t* seq_lens, int num_seqs, int num_heads,

@@ -18,8 +18,22 @@ int decode_mma_dispatch_e4m3(int D, int BS, int G, int HG, const MmaOp& op);
 int decode_mma_dispatch_e5m2(int D, int BS, int G, int HG, const MmaOp& op);
 int decode_mma_dispatch_i8(int D, int BS, int G, int HG, const MmaOp& op);
 
+int decode_mma_heads_dispatch_bf16(int D, int BS, int G, int HG, const MmaOp& op);
+int decode_mma_heads_dispatch_e4m3(int D, int BS, int G, int HG, const MmaOp& op);
+int decode_mma_heads_dispatch_e5m2(int D, int BS, int G, int HG, const MmaOp& op);
+int decode_mma_heads_dispatch_i8(int D, int BS, int G, int HG, const MmaOp& op);
+
 int decode_mma_op(int kv_dtype, int D, int BS, int G, int HG, const MmaOp& op)
 {
+    if (op.kind == MmaOp::kLaunchPerHead || op.kind == MmaOp::kPerHeadOccupancy) {
+        switch (kv_dtype) {
+        case PKV_BF16: return decode_mma_heads_dispatch_bf16(D, BS, G, HG, op);
+        case PKV_FP8_E4M3: return decode_mma_heads_dispatch_e4m3(D, BS, G, HG, op);
+        case PKV_FP8_E5M2: return decode_mma_heads_dispatch_e5m2(D, BS, G, HG, op);
+        case PKV_INT8: return decode_mma_heads_dispatch_i8(D, BS, G, HG, op);
+        default: return PKV_ERR_DTYPE;
+        }
+    }
     if (kv_dtype == PKV_BF16)
         return decode_mma_dispatch_bf16(D, BS, G, HG, op);
     if (kv_dtype == PKV_FP8_E4M3)

@@ -274,7 +274,9 @@ __device__ __forceinline__ size_t query_row(const DecodeParams& p, int s, int he
 // PFX: the prefix pass of a shared-prefix decode. A unit is one KV head of one shared block of a
 // group (HG = 1) and the kNT = 4 consumer warps take its 32 query columns (the group's members x
 // their query heads), 8 each, against the same staged K/V tile.
-template <class KV, int D, int BS, int G, int HG, bool PFX = false>
+// PH: every KV head of a unit is resolved for itself by the producer (UnitHead): its block of a
+// sparse decode, its scales of a cache with block scales.
+template <class KV, int D, int BS, int G, int HG, bool PFX = false, bool PH = false>
 struct MmaCfg {
     // products: bf16 caches in bf16 MMA; 8-bit codes widened exactly to f16 (widen_halves) for f16 MMA,
     // q scaled per column by a power of two into f16's range; INT8 q.K on integer MMA (K codes as
@@ -294,6 +296,8 @@ struct MmaCfg {
     static constexpr int kNT = PFX ? 4 : 1;                   // column tiles (warps) per KV head
     static constexpr int W = HG * kNT;                        // consumer warps
     static constexpr int kThreads = (W + 1) * 32;
+    static constexpr int kHeadBytes = 2 * kRowBytes * BS;     // one KV head's part of a stage
+    static constexpr int kSide = PH ? HG * 16 : 0;            // a stage's UnitHead entries
     // CTAs per SM: E4M3 tiles (16 KB stages) take three, for 12 consumer warps per SM to hide the
     // widening chain's latency; the same ~192 KB of stages per SM stay in flight either way
     static constexpr int kCtasPerSM = (KV::kBytes == 1 && kStage <= 16384) ? 3 : 2;
@@ -302,7 +306,24 @@ struct MmaCfg {
     static_assert(kRows <= 256, "TMA box height");
     static_assert(KV::kBytes == 2 || D == 128, "8-bit MMA tiles: one 128-byte box across head_dim");
     static_assert(!PFX || (HG == 1 && G == 8), "prefix pass: one KV head per unit, 8 columns per warp");
+    static_assert(!PFX || !PH, "the prefix pass reads whole units");
 };
+
+// What the producer tells the consumer warp of one KV head about its tile (one per stage and head).
+// Block scales: value = code * scale with a scale per tile, so a tile's scores are s = ks (q.K) and
+// its output weights are vs p. The accumulators hold 2^(s + log2 vs - m), a number of the size of
+// the tile's share of the output whatever its scale, which keeps f16 weights clear of its
+// subnormals; m is the running maximum of s + log2 vs, and the sum of the weights themselves takes
+// 2^(s + log2 vs - m) / vs. Scales per tensor stay outside (ks = vs = 1).
+struct __align__(16) UnitHead {
+    int valid;      // tokens of the tile that exist (0: none, or no tile)
+    float ks;
+    float log2_vs;
+    float inv_vs;
+};
+// V scales are taken within 2^-50 .. 2^50 (the append's own range): 2^(s + log2 vs - m) / vs then
+// loses nothing above 2^-26 of the sum.
+constexpr float kBlockScaleLo = 8.8817841970012523e-16f, kBlockScaleHi = 1.125899906842624e15f;
 
 // Byte offset of the 16-byte chunk `c` (0..7) of box row `r` in a 128B-swizzled box.
 __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
@@ -337,6 +358,8 @@ __device__ __forceinline__ int stream_tokens(const DecodeParams& p, int s, int B
             skip = skip < 0 ? 0 : L / BS;
         }
     }
+    if (p.selected != nullptr)   // as many units as blocks are listed; how full each is, the unit says
+        return min((L + BS - 1) / BS, p.sel_width) * BS;
     return L - skip * BS;
 }
 
@@ -421,12 +444,13 @@ __device__ __forceinline__ Chunks make_chunks(int U, int R, int tail_chunks, int
 
 // ------------------------------------------------------------------ kernel
 
-template <class KV, class QT, int D, int BS, int G, int HG, bool PFX = false>
-__global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX>::kThreads, MmaCfg<KV, D, BS, G, HG, PFX>::kCtasPerSM)
+template <class KV, class QT, int D, int BS, int G, int HG, bool PFX = false, bool PH = false>
+__global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
+                                  MmaCfg<KV, D, BS, G, HG, PFX, PH>::kCtasPerSM)
     paged_decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                             const DecodeParams p)
 {
-    using C = MmaCfg<KV, D, BS, G, HG, PFX>;
+    using C = MmaCfg<KV, D, BS, G, HG, PFX, PH>;
     constexpr int W = C::W;
     constexpr bool F16 = C::kF16;
     constexpr bool I8 = C::kI8;
@@ -439,7 +463,8 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX>::kThreads, MmaCf
 
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* stages = smem;                                                    // [S][kStage], 1024-aligned
-    uint64_t* full = reinterpret_cast<uint64_t*>(stages + (size_t)S * C::kStage);
+    UnitHead* side = reinterpret_cast<UnitHead*>(stages + (size_t)S * C::kStage);   // [S][HG] when PH
+    uint64_t* full = reinterpret_cast<uint64_t*>(stages + (size_t)S * (C::kStage + C::kSide));
     uint64_t* empty = full + S;
     int* skip = reinterpret_cast<int*>(empty + S);
     volatile int* abort_flag = skip + S;
@@ -551,6 +576,137 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX>::kThreads, MmaCf
                 }
                 return (phys * Hkv + hg * HG) * BS;
             };
+            if constexpr (PH) {
+                // lane l resolves every KV head of unit (batch + l): its block (of the head's list, or
+                // the unit's own), the tokens that exist in it and its scales
+                struct Heads {
+                    int row[HG], valid[HG];
+                    float ks[HG], vs[HG];
+                };
+                auto resolve = [&](int kk) -> Heads {
+                    Heads u;
+#pragma unroll
+                    for (int w = 0; w < HG; ++w) {
+                        u.row[w] = -1;
+                        u.valid[w] = 0;
+                        u.ks[w] = u.vs[w] = 1.f;
+                    }
+                    if (kk >= nunits)
+                        return u;
+                    const int x = cb + kk;
+                    const int s = find_seq(prefix, p.num_seqs, x);
+                    const int nb = (prefix[s + 1] - prefix[s]) / NHG;
+                    const int r = x - prefix[s];
+                    const int hg = r / nb, i = r - hg * nb;
+                    int L = p.seq_lens[s];
+                    L = L > capacity ? capacity : L;
+                    const int blocks = (L + BS - 1) / BS;
+                    int j[HG];
+#pragma unroll
+                    for (int w = 0; w < HG; ++w)
+                        j[w] = p.selected == nullptr
+                                   ? i
+                                   : __ldg(p.selected + ((long long)s * Hkv + hg * HG + w) * p.sel_width + i);
+#pragma unroll
+                    for (int w = 0; w < HG; ++w) {
+                        if (j[w] >= blocks)
+                            atomicOr(p.err, PKV_DEVERR_SELECTION);
+                        if (j[w] < 0 || j[w] >= blocks)
+                            j[w] = -1;
+                        else
+                            u.row[w] = __ldg(p.block_tables + (long long)s * p.max_blocks_per_seq + j[w]);
+                    }
+#pragma unroll
+                    for (int w = 0; w < HG; ++w) {
+                        const int phys = u.row[w];
+                        u.row[w] = -1;
+                        if (j[w] < 0)
+                            continue;
+                        if (phys < 0 || phys >= p.num_blocks) {
+                            atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
+                            continue;
+                        }
+                        const int tile = phys * Hkv + hg * HG + w;
+                        u.row[w] = tile * BS;
+                        u.valid[w] = min(BS, L - j[w] * BS);
+                        if (KV::kBytes == 1 && p.k_block_scales != nullptr) {
+                            u.ks[w] = __ldg(p.k_block_scales + tile);
+                            u.vs[w] = __ldg(p.v_block_scales + tile);
+                        }
+                    }
+                    return u;
+                };
+                Heads now = resolve(lane), ahead = resolve(32 + lane);
+                for (int k0 = 0; k0 < nunits && !aborted; k0 += 32) {
+                    if (k0 > 0) {
+                        now = ahead;
+                        ahead = resolve(k0 + 32 + lane);
+                    }
+                    const int cnt = min(32, nunits - k0);
+                    for (int i = 0; i < cnt && !aborted; ++i, ++k) {
+                        const int st = k % S;
+                        // lane w takes head w's entry
+                        int row = -1, valid = 0;
+                        float ks = 1.f, vs = 1.f;
+#pragma unroll
+                        for (int w = 0; w < HG; ++w) {
+                            const int r = __shfl_sync(kFullMask, now.row[w], i), n = __shfl_sync(kFullMask, now.valid[w], i);
+                            const float a = __shfl_sync(kFullMask, now.ks[w], i), b = __shfl_sync(kFullMask, now.vs[w], i);
+                            if (lane == w) {
+                                row = r;
+                                valid = n;
+                                ks = a;
+                                vs = b;
+                            }
+                        }
+                        if (lane == 0) {
+                            if (*abort_flag) {
+                                aborted = true;
+                            } else if (k >= S && !mbar_wait_bounded(&empty[st], ((k / S) - 1) & 1)) {
+                                aborted = true;
+                                *abort_flag = 1;
+                                atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+                            }
+                        }
+                        aborted = __shfl_sync(kFullMask, aborted ? 1 : 0, 0) != 0;
+                        if (aborted)
+                            break;
+                        const unsigned live = __ballot_sync(kFullMask, row >= 0);
+                        if (lane < HG) {
+                            vs = fminf(fmaxf(vs, kBlockScaleLo), kBlockScaleHi);
+                            UnitHead u;
+                            u.valid = valid;
+                            u.ks = ks;
+                            u.log2_vs = log2f(vs);
+                            u.inv_vs = 1.0f / vs;
+                            side[st * HG + lane] = u;
+                        }
+                        __syncwarp();   // the entries, before the arrival that publishes them
+                        uint8_t* dst = stages + (size_t)st * C::kStage;
+                        if (lane == 0) {
+                            skip[st] = 0;
+                            if (live == 0u)
+                                mbar_arrive(&full[st]);
+                            else
+                                mbar_arrive_expect_tx(&full[st], __popc(live) * C::kHeadBytes);
+                        }
+                        issued = k + 1;
+                        __syncwarp();
+                        if (row >= 0) {   // one box of block_size rows per 128 bytes of the head's tile
+#pragma unroll
+                            for (int bx = 0; bx < C::kBoxes; ++bx) {
+                                uint8_t* at = dst + bx * C::kBoxBytes + lane * (BS * 128);
+                                tma_load_2d(at, &kmap, bx * C::kBoxCols, row, &full[st]);
+                                tma_load_2d(at + C::kHalf, &vmap, bx * C::kBoxCols, row, &full[st]);
+                            }
+                        }
+                    }
+                }
+                cur = __shfl_sync(kFullMask, nxt, 0);
+                if (lane == 0 && cur < ch.C)
+                    nxt = ch.R + atomicAdd(p.chunk_ctr, 1);
+                continue;
+            }
             int cur_app, ahead_app;
             int cur_row = locate(lane, cur_app), ahead = locate(32 + lane, ahead_app);
             for (int k0 = 0; k0 < nunits && !aborted; k0 += 32) {
@@ -786,7 +942,12 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX>::kThreads, MmaCf
                     ok = false;
                 }
                 const int jb = x - stream_begin;         // logical block
-                const int valid = min(BS, L - jb * BS);
+                int valid = min(BS, L - jb * BS);
+                UnitHead uh = {};
+                if constexpr (PH) {
+                    uh = side[st * HG + warp];
+                    valid = uh.valid;
+                }
                 bool released = false;
                 if (ok && skip[st] == 0 && valid > 0) {
                     const uint32_t kbase = smem_addr(stages + (size_t)st * C::kStage);
@@ -881,12 +1042,24 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX>::kThreads, MmaCf
                         }
                         // sc: (token g | g+8) x (heads 2t, 2t+1), in log2 units after the scale
                         // positions in the sequence of rows g and g + 8
-                        const int tok0 = jb * BS + tt * 16 + (F16 ? tok_of_row(g) : g);
-                        const int tok8 = jb * BS + tt * 16 + (F16 ? tok_of_row(g + 8) : g + 8);
-                        sc[0] = (tok0 < lim0) ? sc[0] * qk0 : -INFINITY;
-                        sc[1] = (tok0 < lim1) ? sc[1] * qk1 : -INFINITY;
-                        sc[2] = (tok8 < lim0) ? sc[2] * qk0 : -INFINITY;
-                        sc[3] = (tok8 < lim1) ? sc[3] * qk1 : -INFINITY;
+                        if constexpr (PH) {   // rows of the tile instead of positions in the sequence
+                            const int row0_ = tt * 16 + (F16 ? tok_of_row(g) : g);
+                            const int row8_ = tt * 16 + (F16 ? tok_of_row(g + 8) : g + 8);
+                            const int n0 = 2 * t < G ? valid : 0, n1 = 2 * t + 1 < G ? valid : 0;
+                            const float f0 = F16 ? qk0 * uh.ks : qk0, f1 = F16 ? qk1 * uh.ks : qk1;
+                            const float add = F16 ? uh.log2_vs : 0.f;
+                            sc[0] = (row0_ < n0) ? fmaf(sc[0], f0, add) : -INFINITY;
+                            sc[1] = (row0_ < n1) ? fmaf(sc[1], f1, add) : -INFINITY;
+                            sc[2] = (row8_ < n0) ? fmaf(sc[2], f0, add) : -INFINITY;
+                            sc[3] = (row8_ < n1) ? fmaf(sc[3], f1, add) : -INFINITY;
+                        } else {
+                            const int tok0 = jb * BS + tt * 16 + (F16 ? tok_of_row(g) : g);
+                            const int tok8 = jb * BS + tt * 16 + (F16 ? tok_of_row(g + 8) : g + 8);
+                            sc[0] = (tok0 < lim0) ? sc[0] * qk0 : -INFINITY;
+                            sc[1] = (tok0 < lim1) ? sc[1] * qk1 : -INFINITY;
+                            sc[2] = (tok8 < lim0) ? sc[2] * qk0 : -INFINITY;
+                            sc[3] = (tok8 < lim1) ? sc[3] * qk1 : -INFINITY;
+                        }
                         // The reference moves only when some score passes it by the slack; each lane
                         // tests its own scores first, so the butterfly max runs only when one does
                         // (same result as reducing first: the tile max passes iff some lane's does).
@@ -917,8 +1090,13 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX>::kThreads, MmaCf
                         pr[1] = (sc[1] == -INFINITY) ? 0.f : fast_exp2(sc[1] - m[1]);
                         pr[2] = (sc[2] == -INFINITY) ? 0.f : fast_exp2(sc[2] - m[0]);
                         pr[3] = (sc[3] == -INFINITY) ? 0.f : fast_exp2(sc[3] - m[1]);
-                        l[0] += pr[0] + pr[2];
-                        l[1] += pr[1] + pr[3];
+                        if constexpr (PH && F16) {
+                            l[0] = fmaf(pr[0] + pr[2], uh.inv_vs, l[0]);
+                            l[1] = fmaf(pr[1] + pr[3], uh.inv_vs, l[1]);
+                        } else {
+                            l[0] += pr[0] + pr[2];
+                            l[1] += pr[1] + pr[3];
+                        }
                         const int srcA = (2 * t) * 4 + (g >> 1), srcB = (2 * t + 1) * 4 + (g >> 1);
                         uint32_t pb0, pb1;
                         {
@@ -1362,13 +1540,13 @@ inline int launch_merge_pdl(const void* kern, void** args, int grid, size_t smem
     return cudaLaunchKernelExC(&cfg, kern, args) == cudaSuccess ? PKV_OK : PKV_ERR_LAUNCH;
 }
 
-template <class KV, class QT, int D, int BS, int G, int HG, bool PFX = false>
+template <class KV, class QT, int D, int BS, int G, int HG, bool PFX = false, bool PH = false>
 struct MmaLauncher {
-    using C = MmaCfg<KV, D, BS, G, HG, PFX>;
+    using C = MmaCfg<KV, D, BS, G, HG, PFX, PH>;
 
     static size_t smem_bytes(int num_seqs, int S)
     {
-        return (size_t)S * C::kStage + (size_t)S * (8 + 8 + 4) + 16 + 2 * kChunkRing * 4 + (size_t)(num_seqs + 1) * 4 + 64;
+        return (size_t)S * (C::kStage + C::kSide) + (size_t)S * (8 + 8 + 4) + 16 + 2 * kChunkRing * 4 + (size_t)(num_seqs + 1) * 4 + 64;
     }
 
     // Ring depth: the SM's shared memory split between kCtasPerSM CTAs (~96 KB or ~64 KB of stages).
@@ -1376,12 +1554,12 @@ struct MmaLauncher {
     {
         const long long budget = kMaxSmemPerBlock / C::kCtasPerSM - 1024;
         const long long room = budget - 16 - 2 * kChunkRing * 4 - (long long)(num_seqs + 1) * 4 - 64;
-        long long S = room / (C::kStage + 20);
+        long long S = room / (C::kStage + C::kSide + 20);
         if (S > 8)
             S = 8;
         if (S < 2) {   // many sequences: fall back to one CTA per SM
             S = ((long long)kMaxSmemPerBlock - 1024 - 16 - 2 * kChunkRing * 4 - (long long)(num_seqs + 1) * 4 - 64) /
-                (C::kStage + 20);
+                (C::kStage + C::kSide + 20);
             if (S > 8)
                 S = 8;
         }
@@ -1393,7 +1571,7 @@ struct MmaLauncher {
         const int S = stages(num_seqs);
         if (S < 2)
             return 0;
-        auto kern = paged_decode_mma_kernel<KV, QT, D, BS, G, HG, PFX>;
+        auto kern = paged_decode_mma_kernel<KV, QT, D, BS, G, HG, PFX, PH>;
         const size_t smem = smem_bytes(num_seqs, S);
         if (!ensure_smem_attribute((const void*)kern, smem))
             return 0;
@@ -1415,15 +1593,17 @@ struct MmaLauncher {
         if constexpr (KV::kBytes == 1)
             kvdt = KV::kInt8 ? PKV_INT8 : KV::kFmt == __NV_E5M2 ? PKV_FP8_E5M2 : PKV_FP8_E4M3;
         CUtensorMap kmap, vmap;
-        if (!make_cache_tensormap(&kmap, p.k_cache, kvdt, D, rows, C::kRows) ||
-            !make_cache_tensormap(&vmap, p.v_cache, kvdt, D, rows, C::kRows))
+        const int box_rows = PH ? BS : C::kRows;   // PH: one head's rows at a time
+        if (!make_cache_tensormap(&kmap, p.k_cache, kvdt, D, rows, box_rows) ||
+            !make_cache_tensormap(&vmap, p.v_cache, kvdt, D, rows, box_rows))
             return PKV_ERR_LAUNCH;
-        auto kern = paged_decode_mma_kernel<KV, QT, D, BS, G, HG, PFX>;
+        auto kern = paged_decode_mma_kernel<KV, QT, D, BS, G, HG, PFX, PH>;
         const size_t smem = smem_bytes(p.num_seqs, S);
         if (!ensure_smem_attribute((const void*)kern, smem))
             return PKV_ERR_LAUNCH;
         p.stages_per_warp = S;
-        // 8-bit codes enter the products widened exactly: only the per-tensor scales remain
+        // 8-bit codes enter the products widened exactly: only the per-tensor scales remain (the
+        // caller sets them to 1 where a block's own apply)
         p.q_scale = p.scale * kLog2e * (KV::kBytes == 1 && !p.k_head_scales ? p.k_scale : 1.0f);
         p.v_scale = KV::kBytes == 1 && !p.v_head_scales ? p.v_scale_in : 1.0f;
         cudaLaunchConfig_t cfg = {};

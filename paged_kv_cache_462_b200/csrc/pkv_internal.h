@@ -97,6 +97,14 @@ struct DecodeParams {
     // as soon as its chunks carry this call's stamp. epoch differs from call to call.
     unsigned long long* chunk_done;
     uint32_t epoch;
+    // Sparse decode (null: all blocks): selected[num_seqs][num_kv_heads][sel_width], logical blocks
+    // each KV head attends; a stream's units are its first min(sel_width, ceil(seq_len / block_size))
+    // entries, negative ones are empty.
+    const int32_t* selected;
+    int sel_width;
+    // 8-bit caches with one scale per (block, KV head): [num_blocks][num_kv_heads] (null: the others)
+    const float* k_block_scales;
+    const float* v_block_scales;
 };
 
 // The completion stamp of a chunk in the call with this epoch: the epoch and its complement, a
@@ -108,7 +116,12 @@ __host__ __device__ __forceinline__ unsigned long long chunk_stamp(uint32_t epoc
 
 // One request to the warp-MMA kernels of a shape (decode_mma_dispatch.cuh).
 struct MmaOp {
-    enum Kind { kLaunch = 0, kOccupancy = 1, kLaunchSharedPrefix = 2, kPrefixOccupancy = 3 };
+    // kLaunchPerHead / kPerHeadOccupancy: the variant whose producer resolves every KV head of a unit
+    // for itself (selected blocks, block scales)
+    enum Kind {
+        kLaunch = 0, kOccupancy = 1, kLaunchSharedPrefix = 2, kPrefixOccupancy = 3, kLaunchPerHead = 4,
+        kPerHeadOccupancy = 5
+    };
     int kind;
     const DecodeParams* p;    // the decode (or the shared-prefix suffix pass)
     const DecodeParams* pp;   // the shared-prefix prefix pass (kLaunchSharedPrefix)

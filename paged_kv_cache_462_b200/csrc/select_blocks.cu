@@ -1,0 +1,599 @@
+// The blocks a decode step's queries may need most, for every sequence and KV head
+// (select_blocks).
+//
+//   score(j) = max over the group's query heads of sum_d max(q_d kmax_d, q_d kmin_d)
+//
+// with kmax, kmin the block's key bounds: no key of block j has a larger product with the query.
+// Kept are the first num_sink and the last num_recent blocks and the highest scores of the rest,
+// ties to the lowest index, in ascending order.
+//
+// As q_d kmax_d wins where q_d > 0 and q_d kmin_d where q_d < 0, the sum is q+ . kmax + q- . kmin
+// with q+ = max(q, 0), q- = min(q, 0): two dot products, for eight query columns at once on the
+// warp's tensor cores (m16n8k16: 16 blocks x 8 columns). A lane takes the bounds in 16-byte pieces
+// straight into A fragments: the order of d within a product is free, and q is loaded in the same
+// one. Bound: HBM, 4 * head_dim bytes per block and KV head.
+//
+// fp32 sums cannot tell apart scores that lie closer than their rounding, and a wrong choice is a
+// wrong block. So each product of 16 terms is its own MMA, the partial sums are added in fp32, and
+// with A = sum |q_d k_d| every score is within 2^-17 A of the exact one (an MMA's truncations stay
+// under 17 * 2^-23 of its own |terms|, 2 head_dim / 16 <= 16 fp32 additions under 2^-24 A each).
+// Blocks further than that from the border are decided by the fp32 score; those within it are
+// scored again in fp64, where products of bf16 numbers and their sums are exact but for terms
+// 2^-30 apart. A block whose score is not finite ranks first.
+//
+// One launch: a CTA scores some blocks of one (sequence, KV head); the last of a stream's CTAs to
+// arrive (a counter in the workspace, left at zero) selects among them.
+#include <cstdint>
+
+#include "device.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kSelThreads = 256;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelTile = 16 * kSelWarps;      // blocks a CTA scores at a time
+constexpr int kSelSmemKeys = 8192;            // streams of up to this many blocks are selected in shared memory
+constexpr float kSelError = 7.62939453125e-06f;   // 2^-17
+constexpr uint32_t kChosen = 0xffffffffu;
+// (sequence, KV head) pairs of a call; their counters have this room whatever the call's sizes, so
+// that calls of other sizes, whose scores lie behind it, never write there
+constexpr long long kSelMaxStreams = 1ll << 18;
+
+struct SelectArgs {
+    int32_t* selected;            // [num_seqs][num_kv_heads][keep]
+    const __nv_bfloat16* q;       // [num_seqs][num_heads][D]
+    const __nv_bfloat16* bounds;  // [num_blocks][num_kv_heads][2][D]
+    const int32_t* block_tables;
+    const int32_t* seq_lens;
+    int32_t* err;
+    int32_t* arrived;             // [streams], zero between calls
+    float* magnitude;             // [streams][chunks]: largest A of a chunk
+    float* scores;                // [streams][max_blocks]
+    int32_t* near_list;           // [streams][max_blocks]: blocks near the border
+    double* near_score;           // [streams][max_blocks]
+    int num_heads, num_kv_heads, max_blocks, num_blocks, block_size;
+    int keep, sink, recent, chunks, tiles;   // tiles: of kSelTile blocks, per CTA
+};
+
+__device__ __forceinline__ void mma_bf16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// fp32 order as unsigned order, below kChosen for every finite number.
+__device__ __forceinline__ uint32_t sort_key(float f)
+{
+    const uint32_t u = __float_as_uint(f);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ unsigned long long sort_key(double f)
+{
+    const unsigned long long u = (unsigned long long)__double_as_longlong(f);
+    return u >> 63 ? ~u : u | 0x8000000000000000ull;
+}
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+
+__device__ __forceinline__ int block_sum(int v, int* scratch)
+{
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+        v += __shfl_xor_sync(kFullMask, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0)
+        scratch[threadIdx.x >> 5] = v;
+    __syncthreads();
+    int s = 0;
+#pragma unroll
+    for (int i = 0; i < kSelWarps; ++i)
+        s += scratch[i];
+    return s;
+}
+
+// Exclusive sum over the CTA's threads in order; `total` the sum of all.
+__device__ __forceinline__ int block_scan(int v, int* scratch, int& total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFullMask, x, o);
+        if (lane >= o)
+            x += y;
+    }
+    __syncthreads();
+    if (lane == 31)
+        scratch[warp] = x;
+    __syncthreads();
+    int base = 0;
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < kSelWarps; ++i) {
+        if (i < warp)
+            base += scratch[i];
+        total += scratch[i];
+    }
+    return base + x - v;
+}
+
+// The exact score of a block (a warp): fp64 sums, the largest over the group's query heads.
+template <int D>
+__device__ __forceinline__ double exact_score(const __nv_bfloat16* q, const __nv_bfloat16* bounds, int group, int lane)
+{
+    constexpr int E = D / 32;
+    double hi[E], lo[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        hi[e] = (double)__bfloat162float(bounds[lane * E + e]);
+        lo[e] = (double)__bfloat162float(bounds[D + lane * E + e]);
+    }
+    double best = 0.0;
+    for (int g = 0; g < group; ++g) {
+        double s = 0.0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const double x = (double)__bfloat162float(q[g * D + lane * E + e]);
+            s = fma(x, x > 0.0 ? hi[e] : lo[e], s);
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1)
+            s += __shfl_xor_sync(kFullMask, s, o);
+        best = g == 0 ? s : fmax(best, s);
+    }
+    return best;
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const SelectArgs p)
+{
+    constexpr int NC = D / 32;           // 16-byte pieces of one bound a lane holds
+    extern __shared__ uint32_t smem_keys[];
+    __shared__ int scratch[kSelWarps];
+    __shared__ float fscratch[kSelWarps];
+    __shared__ int hist[256];
+    __shared__ int bcast[2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int stream = blockIdx.x / p.chunks, chunk = blockIdx.x - stream * p.chunks;
+    const int s = stream / p.num_kv_heads, h = stream - s * p.num_kv_heads;
+    int32_t* out = p.selected + (long long)stream * p.keep;
+
+    int L = __ldg(p.seq_lens + s);
+    const int capacity = p.max_blocks * p.block_size;
+    if (L < 0 || L > capacity) {
+        if (chunk == 0 && h == 0 && tid == 0)
+            atomicOr(p.err, PKV_DEVERR_SEQ_LEN);
+        L = L < 0 ? 0 : capacity;
+    }
+    const int nb = (L + p.block_size - 1) / p.block_size;
+    if (nb <= p.keep) {                  // everything is kept
+        if (chunk == 0)
+            for (int i = tid; i < p.keep; i += kSelThreads)
+                out[i] = i < nb ? i : -1;
+        return;
+    }
+    const int per_cta = kSelTile * p.tiles;
+    const int active = (nb + per_cta - 1) / per_cta;
+    if (chunk >= active)
+        return;
+
+    const __nv_bfloat16* q = p.q + ((long long)s * p.num_heads + (long long)h * G) * D;
+    const int32_t* table = p.block_tables + (long long)s * p.max_blocks;
+    float* scores = p.scores + (long long)stream * p.max_blocks;
+    const int g = lane >> 2, t = lane & 3;
+
+    // ---- scores of this CTA's blocks
+    {
+        uint32_t qp[NC][4], qn[NC][4];   // q+ and q- of column g in the order of the bounds' pieces
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            uint4 u = make_uint4(0u, 0u, 0u, 0u);
+            if (g < G)
+                u = __ldg(reinterpret_cast<const uint4*>(q + (long long)g * D) + 4 * c + t);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+                const __nv_bfloat162 a = __hmax2_nan(x, zero), b = __hmin2_nan(x, zero);
+                qp[c][i] = *reinterpret_cast<const uint32_t*>(&a);
+                qn[c][i] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+        }
+        float mag = 0.f;
+        for (int tile = 0; tile < p.tiles; ++tile) {
+            const int first = chunk * per_cta + tile * kSelTile + warp * 16;
+            if (first >= nb)
+                break;
+            uint4 hi[2][NC], lo[2][NC];
+            bool ok[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int j = first + g + 8 * r;
+                int phys = -1;
+                if (j < nb) {
+                    phys = __ldg(table + j);
+                    if (phys < 0 || phys >= p.num_blocks) {
+                        if (t == 0 && h == 0)
+                            atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
+                        phys = -1;
+                    }
+                }
+                ok[r] = phys >= 0;
+                const uint4* row = reinterpret_cast<const uint4*>(
+                    p.bounds + ((long long)phys * p.num_kv_heads + h) * (2 * D));
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    hi[r][c] = ok[r] ? __ldg(row + 4 * c + t) : make_uint4(0u, 0u, 0u, 0u);
+                    lo[r][c] = ok[r] ? __ldg(row + D / 8 + 4 * c + t) : make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+            float sc[4] = {0.f, 0.f, 0.f, 0.f}, ab[4] = {0.f, 0.f, 0.f, 0.f};
+            auto product = [&](const uint4& x, const uint4& y, const uint32_t (&b)[4], bool minus) {
+                constexpr uint32_t M = 0x7fff7fffu;
+                float c[4];
+                mma_bf16_zero(c, x.x, y.x, x.y, y.y, b[0], b[1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sc[i] += c[i];
+                mma_bf16_zero(c, x.z, y.z, x.w, y.w, b[2], b[3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sc[i] += c[i];
+                mma_bf16_zero(c, x.x & M, y.x & M, x.y & M, y.y & M, b[0], b[1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    ab[i] += minus ? -c[i] : c[i];
+                mma_bf16_zero(c, x.z & M, y.z & M, x.w & M, y.w & M, b[2], b[3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    ab[i] += minus ? -c[i] : c[i];
+            };
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                product(hi[0][c], hi[1][c], qp[c], false);
+                product(lo[0][c], lo[1][c], qn[c], true);
+            }
+            // rows first + g (sc 0, 1) and first + g + 8 (sc 2, 3), columns 2t and 2t + 1
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float best = -INFINITY, a = 0.f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (2 * t + i < G) {
+                        const float x = sc[2 * r + i];
+                        best = fmaxf(best, finite(x) ? x : INFINITY);
+                        a = fmaxf(a, ab[2 * r + i]);
+                    }
+                }
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) {
+                    best = fmaxf(best, __shfl_xor_sync(kFullMask, best, o));
+                    a = fmaxf(a, __shfl_xor_sync(kFullMask, a, o));
+                }
+                if (!ok[r])
+                    best = -INFINITY;    // a bad block id: chosen last
+                else if (finite(best))
+                    mag = fmaxf(mag, a);
+                const int j = first + g + 8 * r;
+                if (t == 0 && j < nb)
+                    scores[j] = best;
+            }
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1)
+            mag = fmaxf(mag, __shfl_xor_sync(kFullMask, mag, o));
+        if (lane == 0)
+            fscratch[warp] = mag;
+    }
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+        float m = 0.f;
+        for (int i = 0; i < kSelWarps; ++i)
+            m = fmaxf(m, fscratch[i]);
+        p.magnitude[(long long)stream * p.chunks + chunk] = m;
+        __threadfence();
+        const int before = atomicAdd(p.arrived + stream, 1);
+        if (before == active - 1)
+            p.arrived[stream] = 0;       // for the next call
+        bcast[0] = before == active - 1;
+    }
+    __syncthreads();
+    if (!bcast[0])
+        return;
+
+    // ---- selection, by the stream's last CTA
+    __threadfence();
+    const bool in_smem = nb <= kSelSmemKeys;
+    uint32_t* keys = in_smem ? smem_keys : reinterpret_cast<uint32_t*>(scores);
+    const int need = p.keep - p.sink - p.recent;   // among blocks [sink, nb - recent), more than `need` of them
+    float mag = 0.f;
+    for (int i = tid; i < active; i += kSelThreads)
+        mag = fmaxf(mag, __ldcg(p.magnitude + (long long)stream * p.chunks + i));
+    uint32_t kmin = 0xffffffffu, kmax = 0u;
+    for (int j = tid; j < nb; j += kSelThreads) {
+        uint32_t k = sort_key(__ldcg(scores + j));
+        if (j < p.sink || j >= nb - p.recent) {
+            k = kChosen;
+        } else {
+            kmin = min(kmin, k);
+            kmax = max(kmax, k);
+        }
+        keys[j] = k;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        mag = fmaxf(mag, __shfl_xor_sync(kFullMask, mag, o));
+        kmin = min(kmin, __shfl_xor_sync(kFullMask, kmin, o));
+        kmax = max(kmax, __shfl_xor_sync(kFullMask, kmax, o));
+    }
+    __shared__ uint32_t range[2][kSelWarps];
+    if (lane == 0) {
+        range[0][warp] = kmin;
+        range[1][warp] = kmax;
+        fscratch[warp] = mag;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSelWarps; ++i) {
+        kmin = min(kmin, range[0][i]);
+        kmax = max(kmax, range[1][i]);
+        mag = fmaxf(mag, fscratch[i]);
+    }
+
+    if (need > 0) {
+        // the key of the need-th largest: 256 equal bins between the smallest and the largest key
+        // left, then the same within the bin it lies in
+        uint32_t lo = kmin, hi = kmax;
+        int rank = need;                 // the rank-th largest of the keys in [lo, hi]
+        for (int pass = 0; pass < 5 && lo < hi; ++pass) {   // each keeps 1/256 of the range
+            const uint32_t span = hi - lo;
+            const int shift = span < 256u ? 0 : 24 - __clz(span);
+            hist[tid] = 0;
+            __syncthreads();
+            for (int j = tid; j < nb; j += kSelThreads) {
+                const uint32_t k = keys[j];
+                if (k >= lo && k <= hi)
+                    atomicAdd(&hist[(k - lo) >> shift], 1);
+            }
+            __syncthreads();
+            int total;
+            // thread i holds bin 255 - i: how many keys lie in higher bins
+            const int mine = hist[255 - tid];
+            const int above = block_scan(mine, scratch, total);
+            if (mine > 0 && above < rank && rank <= above + mine) {
+                bcast[0] = 255 - tid;
+                bcast[1] = rank - above;
+            }
+            __syncthreads();
+            const uint32_t bin = (uint32_t)bcast[0];
+            rank = bcast[1];
+            const uint32_t base = lo + (bin << shift);
+            const uint32_t last = base + ((1u << shift) - 1u);
+            hi = last < base || last > hi ? hi : last;
+            lo = base;
+            __syncthreads();
+        }
+        // blocks whose order against that one the fp32 scores do not settle
+        const uint32_t border = lo;
+        const float f = __uint_as_float(border & 0x80000000u ? border & 0x7fffffffu : ~border);
+        uint32_t up = border, down = border;
+        if (finite(f)) {
+            // two errors (the border's own and the block's) and the rounding of this very sum
+            const float d = 2.f * kSelError * mag + fabsf(f) * 2.4e-7f;
+            up = max(border, sort_key(f + d));
+            down = min(border, sort_key(f - d));
+        }
+        int above = 0, near = 0;
+        for (int j = tid; j < nb; j += kSelThreads) {
+            const uint32_t k = keys[j];
+            above += k > up && k != kChosen;
+            near += k >= down && k <= up;
+        }
+        above = block_sum(above, scratch);
+        near = block_sum(near, scratch);
+        int want = need - above;         // of the `near` ones; 1 <= want <= near
+        const bool all = want == near;
+        uint32_t take = all ? down : up + 1u;        // keys from here on are chosen
+        if (!all) {
+            int32_t* list = p.near_list + (long long)stream * p.max_blocks;
+            double* val = p.near_score + (long long)stream * p.max_blocks;
+            // the near blocks in ascending order
+            const int seg = (nb + kSelThreads - 1) / kSelThreads;
+            const int b = min(nb, tid * seg), e = min(nb, b + seg);
+            int cnt = 0, total;
+            for (int j = b; j < e; ++j)
+                cnt += keys[j] >= down && keys[j] <= up;
+            int at = block_scan(cnt, scratch, total);
+            for (int j = b; j < e; ++j)
+                if (keys[j] >= down && keys[j] <= up)
+                    list[at++] = j;
+            __syncthreads();
+            // blocks without a finite score (bad ids among them) keep their place above or below all
+            for (int i = warp; i < near; i += kSelWarps) {
+                const int j = list[i];
+                const uint32_t k = keys[j];
+                double v;
+                if (k >= sort_key(INFINITY)) {
+                    v = INFINITY;
+                } else if (k <= sort_key(-INFINITY)) {
+                    v = -INFINITY;
+                } else {
+                    const long long tile = (long long)__ldg(table + j) * p.num_kv_heads + h;
+                    v = exact_score<D>(q, p.bounds + tile * (2 * D), G, lane);
+                }
+                if (lane == 0)
+                    val[i] = v;
+            }
+            __syncthreads();
+            // the want-th largest exact score, bit by bit
+            unsigned long long bound = 0ull;
+            for (int bit = 63; bit >= 0; --bit) {
+                const unsigned long long trial = bound | (1ull << bit);
+                int c = 0;
+                for (int i = tid; i < near; i += kSelThreads)
+                    c += sort_key(val[i]) >= trial;
+                if (block_sum(c, scratch) >= want)
+                    bound = trial;
+            }
+            int more = 0;
+            for (int i = tid; i < near; i += kSelThreads)
+                more += sort_key(val[i]) > bound;
+            more = block_sum(more, scratch);
+            want -= more;                // of the ties, in order
+            const int seg2 = (near + kSelThreads - 1) / kSelThreads;
+            const int b2 = min(near, tid * seg2), e2 = min(near, b2 + seg2);
+            int ties = 0;
+            for (int i = b2; i < e2; ++i)
+                ties += sort_key(val[i]) == bound;
+            int rank2 = block_scan(ties, scratch, total);
+            for (int i = b2; i < e2; ++i) {
+                const unsigned long long k = sort_key(val[i]);
+                const bool chosen = k > bound || (k == bound && rank2 < want);
+                rank2 += k == bound;
+                keys[list[i]] = chosen ? kChosen : 0u;
+            }
+            __syncthreads();
+        }
+        // emit in ascending order: chosen keys and those from `take` on
+        const int seg = (nb + kSelThreads - 1) / kSelThreads;
+        const int b = min(nb, tid * seg), e = min(nb, b + seg);
+        int cnt = 0, total;
+        for (int j = b; j < e; ++j)
+            cnt += keys[j] >= take;
+        int at = block_scan(cnt, scratch, total);
+        for (int j = b; j < e; ++j)
+            if (keys[j] >= take && at < p.keep)
+                out[at++] = j;
+    } else {
+        for (int i = tid; i < p.keep; i += kSelThreads)
+            out[i] = i < p.sink ? i : nb - p.keep + i;
+    }
+}
+
+struct SelectLayout {
+    size_t arrived, magnitude, scores, near_list, near_score, bytes;
+};
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// chunks of the widest grid (one tile per CTA)
+SelectLayout select_layout(long long streams, long long max_blocks)
+{
+    SelectLayout l;
+    const size_t chunks = (size_t)((max_blocks + kSelTile - 1) / kSelTile);
+    l.arrived = kWorkspaceHeader;
+    l.magnitude = l.arrived + (size_t)kSelMaxStreams * 4;
+    l.scores = l.magnitude + up256((size_t)streams * chunks * 4);
+    l.near_list = l.scores + up256((size_t)streams * max_blocks * 4);
+    l.near_score = l.near_list + up256((size_t)streams * max_blocks * 4);
+    l.bytes = l.near_score + up256((size_t)streams * max_blocks * 8);
+    return l;
+}
+
+bool select_sizes_ok(int num_seqs, int num_kv_heads, int max_blocks)
+{
+    return num_seqs >= 0 && num_seqs <= kMaxSeqs && num_kv_heads > 0 && max_blocks > 0 &&
+           (long long)num_seqs * num_kv_heads <= kSelMaxStreams && (long long)num_seqs * num_kv_heads * max_blocks < (1ll << 31);
+}
+
+template <int D, int G>
+int launch_select(const SelectArgs& p, int num_seqs, cudaStream_t stream)
+{
+    auto kern = select_blocks_kernel<D, G>;
+    const int n = p.max_blocks < kSelSmemKeys ? p.max_blocks : kSelSmemKeys;
+    const long long grid = (long long)num_seqs * p.num_kv_heads * p.chunks;
+    kern<<<(unsigned)grid, kSelThreads, (size_t)n * 4, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_LAUNCH;
+}
+
+template <int D>
+int select_by_group(int group, const SelectArgs& p, int num_seqs, cudaStream_t stream)
+{
+    switch (group) {
+    case 1: return launch_select<D, 1>(p, num_seqs, stream);
+    case 2: return launch_select<D, 2>(p, num_seqs, stream);
+    case 4: return launch_select<D, 4>(p, num_seqs, stream);
+    case 5: return launch_select<D, 5>(p, num_seqs, stream);
+    case 8: return launch_select<D, 8>(p, num_seqs, stream);
+    default: return PKV_ERR_SHAPE;
+    }
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+PKV_API size_t pkv_select_workspace_size(int num_seqs, int num_kv_heads, int max_blocks_per_seq)
+{
+    if (!select_sizes_ok(num_seqs, num_kv_heads, max_blocks_per_seq))
+        return 0;
+    return select_layout((long long)num_seqs * num_kv_heads, max_blocks_per_seq).bytes;
+}
+
+PKV_API int select_blocks(int32_t* selected, const void* q, const void* key_bounds, const int32_t* block_tables,
+                          const int32_t* seq_lens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                          int block_size, int max_blocks_per_seq, int num_blocks, int num_selected,
+                          int num_sink_blocks, int num_recent_blocks, void* workspace, size_t workspace_bytes,
+                          void* stream)
+{
+    if (!select_sizes_ok(num_seqs, num_kv_heads, max_blocks_per_seq) || num_heads <= 0 ||
+        num_heads % num_kv_heads != 0 || (head_dim != 64 && head_dim != 128) ||
+        (block_size != 8 && block_size != 16 && block_size != 32) || num_blocks <= 0 ||
+        (long long)max_blocks_per_seq * block_size >= (1ll << 31) || num_selected < 1 || num_sink_blocks < 0 ||
+        num_recent_blocks < 0 || (long long)num_sink_blocks + num_recent_blocks > num_selected ||
+        (long long)num_seqs * num_kv_heads * num_selected >= (1ll << 31))
+        return PKV_ERR_SHAPE;
+    const int group = num_heads / num_kv_heads;
+    if (group != 1 && group != 2 && group != 4 && group != 5 && group != 8)
+        return PKV_ERR_SHAPE;
+    if (num_seqs == 0)
+        return PKV_OK;
+    if (!selected || !q || !key_bounds || !block_tables || !seq_lens)
+        return PKV_ERR_NULL;
+    const long long streams = (long long)num_seqs * num_kv_heads;
+    const SelectLayout l = select_layout(streams, max_blocks_per_seq);
+    if (!workspace || workspace_bytes < l.bytes)
+        return PKV_ERR_WORKSPACE;
+    auto off16 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) != 0; };
+    if (off16(q) || off16(key_bounds) || off16(workspace))
+        return PKV_ERR_SHAPE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    SelectArgs p{};
+    p.selected = selected;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.bounds = static_cast<const __nv_bfloat16*>(key_bounds);
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.err = reinterpret_cast<int32_t*>(ws);
+    p.arrived = reinterpret_cast<int32_t*>(ws + l.arrived);
+    p.magnitude = reinterpret_cast<float*>(ws + l.magnitude);
+    p.scores = reinterpret_cast<float*>(ws + l.scores);
+    p.near_list = reinterpret_cast<int32_t*>(ws + l.near_list);
+    p.near_score = reinterpret_cast<double*>(ws + l.near_score);
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    p.keep = num_selected;
+    p.sink = num_sink_blocks;
+    p.recent = num_recent_blocks;
+    p.tiles = 1;
+    p.chunks = (max_blocks_per_seq + kSelTile - 1) / kSelTile;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return head_dim == 128 ? select_by_group<128>(group, p, num_seqs, st) : select_by_group<64>(group, p, num_seqs, st);
+}
+
+}  // extern "C"
