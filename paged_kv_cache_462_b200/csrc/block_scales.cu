@@ -84,6 +84,34 @@ __device__ __forceinline__ uint2 encode8(const float (&f)[8], float scale, float
     return make_uint2(w[0], w[1]);
 }
 
+// The same for values that no code saturates for (finite ones, |x| <= qmax * scale, a power of two).
+// INT8: x * inv + 1.5 * 2^23 rounds to an integer in the low bits, nearest even, two's complement.
+template <int KVDT>
+__device__ __forceinline__ uint2 encode8_inside(const float (&f)[8], float inv)
+{
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if constexpr (KVDT == PKV_INT8) {
+            uint32_t c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                c[i] = __float_as_uint(fmaf(f[4 * h + i], inv, 12582912.0f));
+            w[h] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+        } else {
+            uint32_t packed = 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                packed |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(
+                              make_float2(f[4 * h + 2 * i] * inv, f[4 * h + 2 * i + 1] * inv), __NV_SATFINITE,
+                              Code<KVDT>::kFmt))
+                          << (16 * i);
+            w[h] = packed;
+        }
+    }
+    return make_uint2(w[0], w[1]);
+}
+
 // Eight codes -> their values in units of the scale, exactly.
 template <int KVDT>
 __device__ __forceinline__ void decode8(uint2 c, float (&f)[8])
@@ -135,6 +163,17 @@ struct Raw8<float> {
         b = __ldg(reinterpret_cast<const float4*>(p) + 1);
     }
     __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    // the largest magnitude's bits, NaN above infinity above the rest
+    __device__ __forceinline__ uint32_t top() const
+    {
+        uint32_t m = 0;
+        float f[8];
+        get(f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
+        return m;
+    }
     __device__ __forceinline__ void get(float (&f)[8]) const
     {
         f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
@@ -146,6 +185,12 @@ struct Raw8<__nv_bfloat16> {
     uint4 a;
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
     __device__ __forceinline__ void clear() { a = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ uint32_t top() const
+    {
+        constexpr uint32_t M = 0x7fff7fffu;
+        const uint32_t m = __vmaxu2(__vmaxu2(a.x & M, a.y & M), __vmaxu2(a.z & M, a.w & M));
+        return max(m << 16, m & 0xffff0000u);
+    }
     __device__ __forceinline__ void get(float (&f)[8]) const
     {
         widen_word(KvBF16{}, a.x, f + 0);
@@ -193,31 +238,43 @@ __global__ void __launch_bounds__(kAppendThreads) append_block_scales_kernel(con
         else
             raw[i].clear();
     }
-    float mx = 0.f;
+    uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        float f[8];
-        raw[i].get(f);
+    for (int i = 0; i < NP; ++i)
+        top = max(top, raw[i].top());
+    top = __reduce_max_sync(kFullMask, top);
+    const bool all_finite = top < 0x7f800000u;
+    float mx = __uint_as_float(top);
+    if (!all_finite) {                   // infinities and NaN set no scale
+        mx = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float a = fabsf(f[e]);
-            mx = a <= 3.402823466e38f ? fmaxf(mx, a) : mx;   // infinities and NaN set no scale
+        for (int i = 0; i < NP; ++i) {
+            float f[8];
+            raw[i].get(f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float a = fabsf(f[e]);
+                mx = a <= 3.402823466e38f ? fmaxf(mx, a) : mx;
+            }
         }
-    }
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1)
-        mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, o));
+        for (int o = 16; o >= 1; o >>= 1)
+            mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, o));
+    }
     const float need = scale_for<KVDT>(mx);
     const float after = fmaxf(before, need);
     const bool power = (__float_as_uint(after) & 0x7fffffu) == 0u;
-    const float inv = power ? 1.0f / after : 0.f;
+    const float inv = power ? __uint_as_float((254u << 23) - __float_as_uint(after)) : 0.f;
+    // below the largest scale no finite value lies beyond the codes
+    const bool inside = all_finite && power && after < __uint_as_float((uint32_t)(kScaleHi + 127) << 23);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const int o = i * RPP + lane / LPR;
         if (o >= begin && o < end) {
             float f[8];
             raw[i].get(f);
-            *reinterpret_cast<uint2*>(tile + o * D) = encode8<KVDT>(f, after, inv);
+            *reinterpret_cast<uint2*>(tile + o * D) =
+                inside ? encode8_inside<KVDT>(f, inv) : encode8<KVDT>(f, after, inv);
         }
     }
     if (begin > 0 && after > before) {   // the scale grew: the older codes in its units

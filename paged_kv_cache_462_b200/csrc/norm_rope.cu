@@ -49,14 +49,27 @@ struct NormRopeArgs {
     float eps, k_scale, v_scale;
 };
 
-// Four consecutive elements as fp32.
-__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p)
-{
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xffff0000u));
-}
+// Four consecutive elements as they lie, widened when they are used.
+template <class TIN>
+struct Raw4;
+template <>
+struct Raw4<float> {
+    float4 u;
+    __device__ __forceinline__ void load(const float* p) { u = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ void clear() { u = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ float4 get() const { return u; }
+};
+template <>
+struct Raw4<__nv_bfloat16> {
+    uint2 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint2*>(p); }
+    __device__ __forceinline__ void clear() { u = make_uint2(0u, 0u); }
+    __device__ __forceinline__ float4 get() const
+    {
+        return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                           __uint_as_float(u.y & 0xffff0000u));
+    }
+};
 
 __device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
 __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x)
@@ -98,15 +111,15 @@ __device__ __forceinline__ float4 times(float4 a, float4 b)
 }
 
 template <class TIN, class TC, int D, __nv_fp8_interpretation_t FMT = __NV_E4M3>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormRopeArgs p)
+__global__ void __launch_bounds__(kNormThreads, sizeof(TIN) == 2 ? 4 : 3) norm_rope_kernel(const NormRopeArgs p)
 {
     constexpr int LPR = D / 8;                    // lanes per row
     constexpr int kGroups = kNormThreads / LPR;   // rows a CTA has at a time
     const int lane = threadIdx.x % LPR, group = threadIdx.x / LPR;
-    const int per_token = p.groups_per_token;
+    const int per_token = p.groups_per_token, first = group % per_token;
     const long long t = (long long)blockIdx.x * (kGroups / per_token) + group / per_token;
     // (shuffles below: whole warps stay together, a group without a token works on nothing)
-    bool live = t < p.num_tokens;
+    const bool real = t < p.num_tokens;
     const int Hq = p.num_heads, Hkv = p.num_kv_heads;
     const int rows = Hq + Hkv + (p.v ? Hkv : 0);
 
@@ -117,12 +130,35 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormRopeA
     const int d0 = split ? 4 * lane : 8 * lane;
     const int d1 = split ? half + 4 * lane : 8 * lane + 4;
 
+    const TIN* qrow = static_cast<const TIN*>(p.q) + t * p.q_stride;
+    const TIN* krow = static_cast<const TIN*>(p.k) + t * p.k_stride;
+    const TIN* vrow = static_cast<const TIN*>(p.v) + t * p.v_stride;
+    Raw4<TIN> a[kNormUnroll], b[kNormUnroll];
+    auto load_rows = [&](int r0) {
+#pragma unroll
+        for (int u = 0; u < kNormUnroll; ++u) {
+            const int r = r0 + u * per_token;
+            if (real && r < rows) {
+                const TIN* x = r < Hq ? qrow + r * D : r < Hq + Hkv ? krow + (r - Hq) * D : vrow + (r - Hq - Hkv) * D;
+                a[u].load(x + d0);
+                b[u].load(x + d1);
+            } else {
+                a[u].clear();
+                b[u].clear();
+            }
+        }
+    };
+    load_rows(first);    // before anything that waits for a load: the rows are what takes time
+
     float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool live = real;
     long long slot = -1;
-    if (live) {
-        const long long pos = p.positions[t];
+    if (real) {
+        const long long pos = __ldg(p.positions + t);
+        if (p.slots)
+            slot = __ldg(p.slots + t);
         if (pos < 0 || pos >= p.num_positions) {
-            if (lane == 0 && group % per_token == 0 && p.err)
+            if (lane == 0 && first == 0 && p.err)
                 atomicOr(p.err, PKV_DEVERR_POSITION);
             live = false;
         } else {
@@ -131,43 +167,30 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormRopeA
                 c = __ldg(reinterpret_cast<const float4*>(cs + 4 * lane));
                 s = __ldg(reinterpret_cast<const float4*>(cs + half + 4 * lane));
             }
-            if (p.slots) {
-                slot = p.slots[t];
-                if (slot >= p.capacity) {
-                    if (lane == 0 && group % per_token == 0 && p.err)
-                        atomicOr(p.err, PKV_DEVERR_SLOT);
-                    slot = -1;
-                }
+            if (slot >= p.capacity) {
+                if (lane == 0 && first == 0 && p.err)
+                    atomicOr(p.err, PKV_DEVERR_SLOT);
+                slot = -1;
             }
         }
     }
-    const float4 qw0 = load4(static_cast<const TIN*>(p.q_weight) + d0);
-    const float4 qw1 = load4(static_cast<const TIN*>(p.q_weight) + d1);
-    const float4 kw0 = load4(static_cast<const TIN*>(p.k_weight) + d0);
-    const float4 kw1 = load4(static_cast<const TIN*>(p.k_weight) + d1);
+    Raw4<TIN> qw0, qw1, kw0, kw1;
+    qw0.load(static_cast<const TIN*>(p.q_weight) + d0);
+    qw1.load(static_cast<const TIN*>(p.q_weight) + d1);
+    kw0.load(static_cast<const TIN*>(p.k_weight) + d0);
+    kw1.load(static_cast<const TIN*>(p.k_weight) + d1);
+    // offset of this token's row of KV head 0 in the caches; heads lie block_size rows apart
+    const long long head_rows = (long long)p.block_size * D;
     const long long blk = slot >= 0 ? slot / p.block_size : 0;
-    const long long off = slot >= 0 ? slot - blk * p.block_size : 0;
+    const long long at = blk * Hkv * head_rows + (slot >= 0 ? slot - blk * p.block_size : 0) * D;
 
-    for (int r0 = group % per_token; r0 - group % per_token < rows; r0 += kNormUnroll * per_token) {
-        float4 a[kNormUnroll], b[kNormUnroll];
+    for (int r0 = first;;) {
 #pragma unroll
         for (int u = 0; u < kNormUnroll; ++u) {
             const int r = r0 + u * per_token;
-            a[u] = b[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (live && r < rows) {
-                const TIN* x = r < Hq ? static_cast<const TIN*>(p.q) + t * p.q_stride + (long long)r * D
-                               : r < Hq + Hkv
-                                   ? static_cast<const TIN*>(p.k) + t * p.k_stride + (long long)(r - Hq) * D
-                                   : static_cast<const TIN*>(p.v) + t * p.v_stride + (long long)(r - Hq - Hkv) * D;
-                a[u] = load4(x + d0);
-                b[u] = load4(x + d1);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kNormUnroll; ++u) {
-            const int r = r0 + u * per_token;
-            float ss = a[u].x * a[u].x + a[u].y * a[u].y + a[u].z * a[u].z + a[u].w * a[u].w + b[u].x * b[u].x +
-                       b[u].y * b[u].y + b[u].z * b[u].z + b[u].w * b[u].w;
+            const float4 xa = a[u].get(), xb = b[u].get();
+            float ss = xa.x * xa.x + xa.y * xa.y + xa.z * xa.z + xa.w * xa.w + xb.x * xb.x + xb.y * xb.y +
+                       xb.z * xb.z + xb.w * xb.w;
 #pragma unroll
             for (int o = 1; o < LPR; o <<= 1)
                 ss += __shfl_xor_sync(kFullMask, ss, o);
@@ -175,17 +198,17 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormRopeA
                 continue;
             if (r >= Hq + Hkv) {   // a V row: only appended
                 if (slot >= 0) {
-                    TC* dst = static_cast<TC*>(p.v_cache) + ((blk * Hkv + (r - Hq - Hkv)) * p.block_size + off) * D;
-                    cache4<TC, FMT>(dst + d0, a[u], p.v_scale);
-                    cache4<TC, FMT>(dst + d1, b[u], p.v_scale);
+                    TC* dst = static_cast<TC*>(p.v_cache) + at + (r - Hq - Hkv) * head_rows;
+                    cache4<TC, FMT>(dst + d0, xa, p.v_scale);
+                    cache4<TC, FMT>(dst + d1, xb, p.v_scale);
                 }
                 continue;
             }
             const float inv = rsqrtf(ss * (1.0f / D) + p.eps);
             const bool is_q = r < Hq;
             const float4 i4 = make_float4(inv, inv, inv, inv);
-            const float4 x = times(times(a[u], i4), is_q ? qw0 : kw0);
-            const float4 y = times(times(b[u], i4), is_q ? qw1 : kw1);
+            const float4 x = times(times(xa, i4), is_q ? qw0.get() : kw0.get());
+            const float4 y = times(times(xb, i4), is_q ? qw1.get() : kw1.get());
             float4 u0 = x, u1 = y;
             if (split) {
                 u0 = make_float4(x.x * c.x - y.x * s.x, x.y * c.y - y.y * s.y, x.z * c.z - y.z * s.z,
@@ -204,11 +227,15 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormRopeA
                 store4(dst + d0, u0);
                 store4(dst + d1, u1);
             } else if (slot >= 0) {
-                TC* dst = static_cast<TC*>(p.k_cache) + ((blk * Hkv + (r - Hq)) * p.block_size + off) * D;
+                TC* dst = static_cast<TC*>(p.k_cache) + at + (r - Hq) * head_rows;
                 cache4<TC, FMT>(dst + d0, u0, p.k_scale);
                 cache4<TC, FMT>(dst + d1, u1, p.k_scale);
             }
         }
+        r0 += kNormUnroll * per_token;
+        if (r0 - first >= rows)
+            break;
+        load_rows(r0);
     }
 }
 

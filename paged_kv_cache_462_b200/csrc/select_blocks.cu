@@ -14,9 +14,9 @@
 // one. Bound: HBM, 4 * head_dim bytes per block and KV head.
 //
 // fp32 sums cannot tell apart scores that lie closer than their rounding, and a wrong choice is a
-// wrong block. So each product of 16 terms is its own MMA, the partial sums are added in fp32, and
-// with A = sum |q_d k_d| every score is within 2^-17 A of the exact one (an MMA's truncations stay
-// under 17 * 2^-23 of its own |terms|, 2 head_dim / 16 <= 16 fp32 additions under 2^-24 A each).
+// wrong block. So the MMAs sum 32 terms at a time, those sums are added in fp32, and with
+// A = sum |q_d k_d| every score is within 2^-17 A of the exact one (the truncations of two chained
+// MMAs stay under 35 * 2^-23 of their own |terms|, 2 head_dim / 32 <= 8 additions under 2^-24 A each).
 // Blocks further than that from the border are decided by the fp32 score; those within it are
 // scored again in fp64, where products of bf16 numbers and their sums are exact but for terms
 // 2^-30 apart. A block whose score is not finite ranks first.
@@ -24,6 +24,7 @@
 // One launch: a CTA scores some blocks of one (sequence, KV head); the last of a stream's CTAs to
 // arrive (a counter in the workspace, left at zero) selects among them.
 #include <cstdint>
+#include <cstdlib>
 
 #include "device.cuh"
 #include "pkv_internal.h"
@@ -68,6 +69,16 @@ __device__ __forceinline__ void mma_bf16_zero(float (&c)[4], uint32_t a0, uint32
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 // fp32 order as unsigned order, below kChosen for every finite number.
 __device__ __forceinline__ uint32_t sort_key(float f)
 {
@@ -96,6 +107,26 @@ __device__ __forceinline__ int block_sum(int v, int* scratch)
     for (int i = 0; i < kSelWarps; ++i)
         s += scratch[i];
     return s;
+}
+
+// Both sums in one exchange.
+__device__ __forceinline__ void block_sum2(int& a, int& b, int2* scratch)
+{
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        a += __shfl_xor_sync(kFullMask, a, o);
+        b += __shfl_xor_sync(kFullMask, b, o);
+    }
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0)
+        scratch[threadIdx.x >> 5] = make_int2(a, b);
+    __syncthreads();
+    a = b = 0;
+#pragma unroll
+    for (int i = 0; i < kSelWarps; ++i) {
+        a += scratch[i].x;
+        b += scratch[i].y;
+    }
 }
 
 // Exclusive sum over the CTA's threads in order; `total` the sum of all.
@@ -157,9 +188,11 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
     constexpr int NC = D / 32;           // 16-byte pieces of one bound a lane holds
     extern __shared__ uint32_t smem_keys[];
     __shared__ int scratch[kSelWarps];
+    __shared__ int2 scratch2[kSelWarps];
+    __shared__ double near_vals[kSelThreads];
     __shared__ float fscratch[kSelWarps];
     __shared__ int hist[256];
-    __shared__ int bcast[2];
+    __shared__ int bcast[3];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int stream = blockIdx.x / p.chunks, chunk = blockIdx.x - stream * p.chunks;
     const int s = stream / p.num_kv_heads, h = stream - s * p.num_kv_heads;
@@ -235,31 +268,23 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
                     lo[r][c] = ok[r] ? __ldg(row + D / 8 + 4 * c + t) : make_uint4(0u, 0u, 0u, 0u);
                 }
             }
-            float sc[4] = {0.f, 0.f, 0.f, 0.f}, ab[4] = {0.f, 0.f, 0.f, 0.f};
-            auto product = [&](const uint4& x, const uint4& y, const uint32_t (&b)[4], bool minus) {
+            // sc: the scores; ab and an: the sums of |q+ kmax| and of -|q- kmin|
+            float sc[4] = {0.f, 0.f, 0.f, 0.f}, ab[4] = {0.f, 0.f, 0.f, 0.f}, an[4] = {0.f, 0.f, 0.f, 0.f};
+            auto product = [&](const uint4& x, const uint4& y, const uint32_t (&b)[4], float (&size)[4]) {
                 constexpr uint32_t M = 0x7fff7fffu;
                 float c[4];
                 mma_bf16_zero(c, x.x, y.x, x.y, y.y, b[0], b[1]);
+                mma_bf16(c, x.z, y.z, x.w, y.w, b[2], b[3]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     sc[i] += c[i];
-                mma_bf16_zero(c, x.z, y.z, x.w, y.w, b[2], b[3]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sc[i] += c[i];
-                mma_bf16_zero(c, x.x & M, y.x & M, x.y & M, y.y & M, b[0], b[1]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    ab[i] += minus ? -c[i] : c[i];
-                mma_bf16_zero(c, x.z & M, y.z & M, x.w & M, y.w & M, b[2], b[3]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    ab[i] += minus ? -c[i] : c[i];
+                mma_bf16(size, x.x & M, y.x & M, x.y & M, y.y & M, b[0], b[1]);
+                mma_bf16(size, x.z & M, y.z & M, x.w & M, y.w & M, b[2], b[3]);
             };
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-                product(hi[0][c], hi[1][c], qp[c], false);
-                product(lo[0][c], lo[1][c], qn[c], true);
+                product(hi[0][c], hi[1][c], qp[c], ab);
+                product(lo[0][c], lo[1][c], qn[c], an);
             }
             // rows first + g (sc 0, 1) and first + g + 8 (sc 2, 3), columns 2t and 2t + 1
 #pragma unroll
@@ -270,7 +295,7 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
                     if (2 * t + i < G) {
                         const float x = sc[2 * r + i];
                         best = fmaxf(best, finite(x) ? x : INFINITY);
-                        a = fmaxf(a, ab[2 * r + i]);
+                        a = fmaxf(a, ab[2 * r + i] - an[2 * r + i]);
                     }
                 }
 #pragma unroll
@@ -351,10 +376,11 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
 
     if (need > 0) {
         // the key of the need-th largest: 256 equal bins between the smallest and the largest key
-        // left, then the same within the bin it lies in
+        // left, then the same within the bin it lies in, until that holds at most one key a thread
         uint32_t lo = kmin, hi = kmax;
         int rank = need;                 // the rank-th largest of the keys in [lo, hi]
-        for (int pass = 0; pass < 5 && lo < hi; ++pass) {   // each keeps 1/256 of the range
+        int in_bin = nb;
+        for (int pass = 0; pass < 5 && lo < hi && in_bin > kSelThreads; ++pass) {
             const uint32_t span = hi - lo;
             const int shift = span < 256u ? 0 : 24 - __clz(span);
             hist[tid] = 0;
@@ -372,15 +398,44 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
             if (mine > 0 && above < rank && rank <= above + mine) {
                 bcast[0] = 255 - tid;
                 bcast[1] = rank - above;
+                bcast[2] = mine;
             }
             __syncthreads();
             const uint32_t bin = (uint32_t)bcast[0];
             rank = bcast[1];
+            in_bin = bcast[2];
             const uint32_t base = lo + (bin << shift);
             const uint32_t last = base + ((1u << shift) - 1u);
             hi = last < base || last > hi ? hi : last;
             lo = base;
             __syncthreads();
+        }
+        if (lo < hi) {                   // rank the keys that are left against one another
+            if (tid == 0)
+                bcast[0] = 0;
+            __syncthreads();
+            for (int j = tid; j < nb; j += kSelThreads) {
+                const uint32_t k = keys[j];
+                if (k >= lo && k <= hi) {
+                    const int at = atomicAdd(&bcast[0], 1);
+                    if (at < kSelThreads)
+                        hist[at] = (int)k;
+                }
+            }
+            __syncthreads();
+            const int n = min(bcast[0], kSelThreads);
+            if (tid < n) {
+                const uint32_t k = (uint32_t)hist[tid];
+                int greater = 0, equal = 0;
+                for (int i = 0; i < n; ++i) {
+                    greater += (uint32_t)hist[i] > k;
+                    equal += (uint32_t)hist[i] == k;
+                }
+                if (greater < rank && rank <= greater + equal)
+                    bcast[1] = (int)k;   // the same key from every thread that holds it
+            }
+            __syncthreads();
+            lo = (uint32_t)bcast[1];
         }
         // blocks whose order against that one the fp32 scores do not settle
         const uint32_t border = lo;
@@ -398,8 +453,7 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
             above += k > up && k != kChosen;
             near += k >= down && k <= up;
         }
-        above = block_sum(above, scratch);
-        near = block_sum(near, scratch);
+        block_sum2(above, near, scratch2);
         int want = need - above;         // of the `near` ones; 1 <= want <= near
         const bool all = want == near;
         uint32_t take = all ? down : up + 1u;        // keys from here on are chosen
@@ -431,37 +485,50 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
                     v = exact_score<D>(q, p.bounds + tile * (2 * D), G, lane);
                 }
                 if (lane == 0)
-                    val[i] = v;
+                    (near <= kSelThreads ? near_vals : val)[i] = v;
             }
             __syncthreads();
-            // the want-th largest exact score, bit by bit
-            unsigned long long bound = 0ull;
-            for (int bit = 63; bit >= 0; --bit) {
-                const unsigned long long trial = bound | (1ull << bit);
-                int c = 0;
+            if (near <= kSelThreads) {   // a few: each is ranked against the others, ties by index
+                if (tid < near) {
+                    const unsigned long long mine = sort_key(near_vals[tid]);
+                    int better = 0;
+                    for (int i = 0; i < near; ++i) {
+                        const unsigned long long k = sort_key(near_vals[i]);
+                        better += k > mine || (k == mine && i < tid);
+                    }
+                    keys[list[tid]] = better < want ? kChosen : 0u;
+                }
+                __syncthreads();
+            } else {
+                // the want-th largest exact score, bit by bit
+                unsigned long long bound = 0ull;
+                for (int bit = 63; bit >= 0; --bit) {
+                    const unsigned long long trial = bound | (1ull << bit);
+                    int c = 0;
+                    for (int i = tid; i < near; i += kSelThreads)
+                        c += sort_key(val[i]) >= trial;
+                    if (block_sum(c, scratch) >= want)
+                        bound = trial;
+                }
+                int more = 0;
                 for (int i = tid; i < near; i += kSelThreads)
-                    c += sort_key(val[i]) >= trial;
-                if (block_sum(c, scratch) >= want)
-                    bound = trial;
+                    more += sort_key(val[i]) > bound;
+                more = block_sum(more, scratch);
+                want -= more;                // of the ties, in order
+                const int seg2 = (near + kSelThreads - 1) / kSelThreads;
+                const int b2 = min(near, tid * seg2), e2 = min(near, b2 + seg2);
+                int ties = 0;
+                for (int i = b2; i < e2; ++i)
+                    ties += sort_key(val[i]) == bound;
+                int rank2 = block_scan(ties, scratch, total);
+                for (int i = b2; i < e2; ++i) {
+                    const unsigned long long k = sort_key(val[i]);
+                    const bool chosen = k > bound || (k == bound && rank2 < want);
+                    rank2 += k == bound;
+                    keys[list[i]] = chosen ? kChosen : 0u;
+                }
+                __syncthreads();
             }
-            int more = 0;
-            for (int i = tid; i < near; i += kSelThreads)
-                more += sort_key(val[i]) > bound;
-            more = block_sum(more, scratch);
-            want -= more;                // of the ties, in order
-            const int seg2 = (near + kSelThreads - 1) / kSelThreads;
-            const int b2 = min(near, tid * seg2), e2 = min(near, b2 + seg2);
-            int ties = 0;
-            for (int i = b2; i < e2; ++i)
-                ties += sort_key(val[i]) == bound;
-            int rank2 = block_scan(ties, scratch, total);
-            for (int i = b2; i < e2; ++i) {
-                const unsigned long long k = sort_key(val[i]);
-                const bool chosen = k > bound || (k == bound && rank2 < want);
-                rank2 += k == bound;
-                keys[list[i]] = chosen ? kChosen : 0u;
-            }
-            __syncthreads();
         }
         // emit in ascending order: chosen keys and those from `take` on
         const int seg = (nb + kSelThreads - 1) / kSelThreads;
@@ -590,8 +657,12 @@ PKV_API int select_blocks(int32_t* selected, const void* q, const void* key_boun
     p.keep = num_selected;
     p.sink = num_sink_blocks;
     p.recent = num_recent_blocks;
-    p.tiles = 1;
-    p.chunks = (max_blocks_per_seq + kSelTile - 1) / kSelTile;
+    // tiles per CTA: up to 4 where the grid stays above six CTAs an SM without them
+    const long long all_tiles = streams * ((max_blocks_per_seq + kSelTile - 1) / kSelTile);
+    const int kTilesEnv = getenv("PKV_T") ? atoi(getenv("PKV_T")) : 4;
+    p.tiles = (int)(all_tiles / (148 * 6));
+    p.tiles = p.tiles < 1 ? 1 : (p.tiles > kTilesEnv ? kTilesEnv : p.tiles);
+    p.chunks = (max_blocks_per_seq + kSelTile * p.tiles - 1) / (kSelTile * p.tiles);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return head_dim == 128 ? select_by_group<128>(group, p, num_seqs, st) : select_by_group<64>(group, p, num_seqs, st);
 }
