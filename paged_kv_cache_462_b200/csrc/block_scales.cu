@@ -20,6 +20,8 @@ namespace pkv {
 namespace {
 
 constexpr int kAppendThreads = 128;
+constexpr int kAppendWarps = kAppendThreads / 32;
+constexpr long long kAppendSplit = 148 * 12;
 constexpr int kScaleLo = -50, kScaleHi = 50;
 
 template <int KVDT>
@@ -147,7 +149,6 @@ struct AppendBlockArgs {
     const int32_t* row_offsets;
     int32_t* err;
     long long k_stride, v_stride;
-    long long work;     // items * num_kv_heads * 2
     int num_tokens, num_seqs, num_kv_heads, max_blocks, num_blocks;
 };
 
@@ -201,101 +202,106 @@ struct Raw8<__nv_bfloat16> {
 };
 
 template <class TIN, int KVDT, int D, int BS>
-__global__ void __launch_bounds__(kAppendThreads) append_block_scales_kernel(const AppendBlockArgs p)
+__global__ void __launch_bounds__(kAppendThreads, BS / (32 / (D / 8)) * sizeof(TIN) <= 16 ? 5 : 3) append_block_scales_kernel(const AppendBlockArgs p)
 {
     constexpr int LPR = D / 8;           // lanes per row, 8 elements each
     constexpr int RPP = 32 / LPR;        // rows a warp reads at a time
     constexpr int NP = BS / RPP;         // passes over a whole block
     const int lane = threadIdx.x & 31;
-    const long long thread = (long long)blockIdx.x * kAppendThreads + threadIdx.x;
-    touched_flag(p.row_offsets, p.seq_lens, p.num_seqs, p.num_tokens, p.max_blocks * BS, thread, p.err);
-    const long long w = thread >> 5;
-    if (w >= p.work)
-        return;
-    const bool is_v = w & 1;
-    const int h = (int)((w >> 1) % p.num_kv_heads);
-    const long long item = (w >> 1) / p.num_kv_heads;
-    // (only the first warp of an item reports its block id)
+    const int warp = threadIdx.x >> 5;
+    if (blockIdx.y == 0)
+        touched_flag(p.row_offsets, p.seq_lens, p.num_seqs, p.num_tokens, p.max_blocks * BS,
+                     (long long)blockIdx.x * kAppendThreads + threadIdx.x, p.err);
+    // (only an item's first warp reports its block id)
     const Touched t = touched_find(p.row_offsets, p.seq_lens, p.block_tables, p.num_seqs, p.num_tokens, BS,
-                                   p.max_blocks, p.num_blocks, item, lane, !is_v && h == 0 ? p.err : nullptr);
+                                   p.max_blocks, p.num_blocks, blockIdx.x, lane,
+                                   blockIdx.y == 0 && warp == 0 ? p.err : nullptr);
     if (t.phys < 0)
         return;
     const int begin = max(0, t.first - t.block * BS);        // this block's new offsets: [begin, end)
     const int end = min(BS, t.len - t.block * BS);
     const long long row0 = (long long)t.row + t.block * BS - t.first;   // row of offset 0 (may be before the call's)
-    const long long stride = is_v ? p.v_stride : p.k_stride;
-    const TIN* src = static_cast<const TIN*>(is_v ? p.v : p.k) + (long long)h * D + (lane % LPR) * 8;
-    uint8_t* tile = (is_v ? p.v_cache : p.k_cache) + ((long long)t.phys * p.num_kv_heads + h) * (BS * D) + (lane % LPR) * 8;
-    float* scale_at = (is_v ? p.v_scales : p.k_scales) + (long long)t.phys * p.num_kv_heads + h;
-    const float before = begin > 0 ? *scale_at : 0.f;
+    // the block's tiles: KV head job / 2, K or V
+    for (int job = blockIdx.y * kAppendWarps + warp; job < 2 * p.num_kv_heads; job += gridDim.y * kAppendWarps) {
+        const bool is_v = job & 1;
+        const int h = job >> 1;
+        const long long stride = is_v ? p.v_stride : p.k_stride;
+        const TIN* src = static_cast<const TIN*>(is_v ? p.v : p.k) + (long long)h * D + (lane % LPR) * 8;
+        uint8_t* tile = (is_v ? p.v_cache : p.k_cache) + ((long long)t.phys * p.num_kv_heads + h) * (BS * D) + (lane % LPR) * 8;
+        float* scale_at = (is_v ? p.v_scales : p.k_scales) + (long long)t.phys * p.num_kv_heads + h;
+        const float before = begin > 0 ? *scale_at : 0.f;
 
-    Raw8<TIN> raw[NP];
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        const int o = i * RPP + lane / LPR;
-        if (o >= begin && o < end)
-            raw[i].load(src + (row0 + o) * stride);
-        else
-            raw[i].clear();
-    }
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < NP; ++i)
-        top = max(top, raw[i].top());
-    top = __reduce_max_sync(kFullMask, top);
-    const bool all_finite = top < 0x7f800000u;
-    float mx = __uint_as_float(top);
-    if (!all_finite) {                   // infinities and NaN set no scale
-        mx = 0.f;
+        Raw8<TIN> raw[NP];
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            float f[8];
-            raw[i].get(f);
+            const int o = i * RPP + lane / LPR;
+            if (o >= begin && o < end)
+                raw[i].load(src + (row0 + o) * stride);
+            else
+                raw[i].clear();
+        }
+        uint32_t top = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float a = fabsf(f[e]);
-                mx = a <= 3.402823466e38f ? fmaxf(mx, a) : mx;
+        for (int i = 0; i < NP; ++i)
+            top = max(top, raw[i].top());
+        top = __reduce_max_sync(kFullMask, top);
+        const bool all_finite = top < 0x7f800000u;
+        float mx = __uint_as_float(top);
+        if (!all_finite) {                   // infinities and NaN set no scale
+            mx = 0.f;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                float f[8];
+                raw[i].get(f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float a = fabsf(f[e]);
+                    mx = a <= 3.402823466e38f ? fmaxf(mx, a) : mx;
+                }
+            }
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1)
+                mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, o));
+        }
+        const float need = scale_for<KVDT>(mx);
+        const float after = fmaxf(before, need);
+        const bool power = (__float_as_uint(after) & 0x7fffffu) == 0u;
+        const float inv = power ? __uint_as_float((254u << 23) - __float_as_uint(after)) : 0.f;
+        // below the largest scale no finite value lies beyond the codes
+        const bool inside = all_finite && power && after < __uint_as_float((uint32_t)(kScaleHi + 127) << 23);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int o = i * RPP + lane / LPR;
+            if (o >= begin && o < end) {
+                float f[8];
+                raw[i].get(f);
+                *reinterpret_cast<uint2*>(tile + o * D) =
+                    inside ? encode8_inside<KVDT>(f, inv) : encode8<KVDT>(f, after, inv);
             }
         }
+        if (begin > 0 && after > before) {   // the scale grew: the older codes in its units
+            for (int o = lane / LPR; o < begin; o += RPP) {
+                float f[8];
+                decode8<KVDT>(*reinterpret_cast<const uint2*>(tile + o * D), f);
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1)
-            mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, o));
-    }
-    const float need = scale_for<KVDT>(mx);
-    const float after = fmaxf(before, need);
-    const bool power = (__float_as_uint(after) & 0x7fffffu) == 0u;
-    const float inv = power ? __uint_as_float((254u << 23) - __float_as_uint(after)) : 0.f;
-    // below the largest scale no finite value lies beyond the codes
-    const bool inside = all_finite && power && after < __uint_as_float((uint32_t)(kScaleHi + 127) << 23);
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        const int o = i * RPP + lane / LPR;
-        if (o >= begin && o < end) {
-            float f[8];
-            raw[i].get(f);
-            *reinterpret_cast<uint2*>(tile + o * D) =
-                inside ? encode8_inside<KVDT>(f, inv) : encode8<KVDT>(f, after, inv);
+                for (int e = 0; e < 8; ++e)
+                    f[e] *= before;
+                *reinterpret_cast<uint2*>(tile + o * D) = encode8<KVDT>(f, after, inv);
+            }
         }
+        if (lane == 0 && !(before == after))
+            *scale_at = after;
     }
-    if (begin > 0 && after > before) {   // the scale grew: the older codes in its units
-        for (int o = lane / LPR; o < begin; o += RPP) {
-            float f[8];
-            decode8<KVDT>(*reinterpret_cast<const uint2*>(tile + o * D), f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                f[e] *= before;
-            *reinterpret_cast<uint2*>(tile + o * D) = encode8<KVDT>(f, after, inv);
-        }
-    }
-    if (lane == 0 && !(before == after))
-        *scale_at = after;
 }
 
 template <class TIN, int KVDT, int D, int BS>
 int launch_append(const AppendBlockArgs& p, cudaStream_t stream)
 {
-    const long long grid = (p.work * 32 + kAppendThreads - 1) / kAppendThreads;
-    append_block_scales_kernel<TIN, KVDT, D, BS><<<(unsigned)grid, kAppendThreads, 0, stream>>>(p);
+    const long long items = touched_items(p.num_tokens, p.num_seqs, BS);
+    // a CTA per block; where there are few, several, so that no warp has two tiles
+    const int jobs = (2 * p.num_kv_heads + kAppendWarps - 1) / kAppendWarps;
+    const int split = items * jobs <= kAppendSplit ? jobs : 1;
+    append_block_scales_kernel<TIN, KVDT, D, BS><<<dim3((unsigned)items, split), kAppendThreads, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_LAUNCH;
 }
 
@@ -371,7 +377,6 @@ extern "C" PKV_API int reshape_and_cache_block_scales(const void* k, const void*
     p.err = device_error;
     p.k_stride = k_stride;
     p.v_stride = v_stride;
-    p.work = touched_items(num_tokens, num_seqs, block_size) * num_kv_heads * 2;
     p.num_tokens = num_tokens;
     p.num_seqs = num_seqs;
     p.num_kv_heads = num_kv_heads;

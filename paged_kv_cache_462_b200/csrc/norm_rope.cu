@@ -12,8 +12,11 @@
 // Layout: a row is held by head_dim / 8 lanes (16 or 8), 8 elements each, as two chunks of four
 // chosen so that both elements of a rotation pair lie in one lane: chunks (4c, rotary/2 + 4c) for
 // half-split pairs, (8c, 8c + 4) for interleaved ones and for the part that is not rotated. The
-// only exchange is the butterfly sum of squares. A CTA takes one token (several when a token has
-// few rows), so that a lane reads its cos and sin once for all its rows.
+// only exchange is the butterfly sum of squares. A thread has up to four rows of a token and the
+// same rows of every token it takes (two or three CTAs an SM, tokens dealt out in turn), so where they
+// go is worked out once and a token's cos and sin serve all of them. A warp of its own brings the
+// rows into a ring of stages by bulk copies, tokens ahead of the arithmetic: a token's rows of q, of
+// k and of v are each one run of memory.
 #include <cstdint>
 #include <type_traits>
 
@@ -45,6 +48,8 @@ struct NormRopeArgs {
     long long capacity;
     int num_tokens, num_heads, num_kv_heads, rotary, num_positions, block_size;
     int interleaved;
+    int block_shift;        // log2 of block_size
+    int stages, stage_bytes;
     int groups_per_token;   // lane groups that share a token's rows (a power of two)
     float eps, k_scale, v_scale;
 };
@@ -57,6 +62,7 @@ struct Raw4<float> {
     float4 u;
     __device__ __forceinline__ void load(const float* p) { u = *reinterpret_cast<const float4*>(p); }
     __device__ __forceinline__ void clear() { u = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = u; }
     __device__ __forceinline__ float4 get() const { return u; }
 };
 template <>
@@ -64,6 +70,7 @@ struct Raw4<__nv_bfloat16> {
     uint2 u;
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint2*>(p); }
     __device__ __forceinline__ void clear() { u = make_uint2(0u, 0u); }
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint2*>(p) = u; }
     __device__ __forceinline__ float4 get() const
     {
         return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
@@ -105,153 +112,351 @@ __device__ __forceinline__ void cache4(TC* p, float4 x, float scale)
     }
 }
 
-__device__ __forceinline__ float4 times(float4 a, float4 b)
+// Four fp32 numbers as two pairs for the packed fp32 instructions (two products or fused
+// multiply-adds each, rounded as the single ones are).
+struct Pairs {
+    unsigned long long lo, hi;
+};
+__device__ __forceinline__ Pairs pairs(float4 x)
 {
-    return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
+    Pairs p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p.lo) : "f"(x.x), "f"(x.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p.hi) : "f"(x.z), "f"(x.w));
+    return p;
+}
+__device__ __forceinline__ float4 singles(Pairs p)
+{
+    float4 x;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x.x), "=f"(x.y) : "l"(p.lo));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x.z), "=f"(x.w) : "l"(p.hi));
+    return x;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b)
+{
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c)
+{
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ Pairs times(Pairs a, Pairs b) { return Pairs{mul2(a.lo, b.lo), mul2(a.hi, b.hi)}; }
+__device__ __forceinline__ Pairs plus_times(Pairs a, Pairs b, Pairs c)   // a b + c
+{
+    return Pairs{fma2(a.lo, b.lo, c.lo), fma2(a.hi, b.hi, c.hi)};
 }
 
-template <class TIN, class TC, int D, __nv_fp8_interpretation_t FMT = __NV_E4M3>
-__global__ void __launch_bounds__(kNormThreads, sizeof(TIN) == 2 ? 4 : 3) norm_rope_kernel(const NormRopeArgs p)
+// Shared memory of a CTA: a ring of stages, each the rows of the tokens a CTA works on at a time, as
+// they lie in memory; the weights in fp32; the ring's barriers.
+template <class TIN, int D>
+struct NormSmem {
+    static constexpr int kBudget = sizeof(TIN) == 2 ? 64 * 1024 : 96 * 1024;   // three or two CTAs an SM
+    static constexpr int kMaxStages = 8;
+    static constexpr int kWeights = 2 * D * 4;
+    static constexpr int kBarriers = 2 * kMaxStages * 8 + 16;
+    static int stages(int stage_bytes)
+    {
+        const int n = kBudget / stage_bytes;
+        return n > kMaxStages ? kMaxStages : n;
+    }
+    static size_t bytes(int stages, int stage_bytes) { return (size_t)stages * stage_bytes + kWeights + kBarriers; }
+};
+
+// WHOLE: half-split pairs over the whole head (rotary == D), what most models use: the chunks' places
+// are known when this is compiled. CACHED: K and V go to the caches.
+template <class TIN, class TC, int D, __nv_fp8_interpretation_t FMT, bool WHOLE, bool CACHED>
+__global__ void __launch_bounds__(kNormThreads + 32, sizeof(TIN) == 2 ? 3 : 2) norm_rope_kernel(const NormRopeArgs p)
 {
     constexpr int LPR = D / 8;                    // lanes per row
     constexpr int kGroups = kNormThreads / LPR;   // rows a CTA has at a time
-    const int lane = threadIdx.x % LPR, group = threadIdx.x / LPR;
-    const int per_token = p.groups_per_token, first = group % per_token;
-    const long long t = (long long)blockIdx.x * (kGroups / per_token) + group / per_token;
-    // (shuffles below: whole warps stay together, a group without a token works on nothing)
-    const bool real = t < p.num_tokens;
+    constexpr int kWarps = kNormThreads / 32;
+    constexpr int kRowBytes = D * sizeof(TIN);
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int S = p.stages;
+    float* weights = reinterpret_cast<float*>(smem + S * p.stage_bytes);          // [2][D]
+    uint64_t* full = reinterpret_cast<uint64_t*>(weights + 2 * D);
+    uint64_t* empty = full + S;
+    volatile int* abort_flag = reinterpret_cast<int*>(empty + S);
+
+    const int per_token = p.groups_per_token, tokens = kGroups / per_token;   // tokens at a time
+    const int stride = gridDim.x * tokens;                                     // from one set to the next
     const int Hq = p.num_heads, Hkv = p.num_kv_heads;
-    const int rows = Hq + Hkv + (p.v ? Hkv : 0);
+    const int rows = Hq + Hkv + (CACHED ? Hkv : 0);
+    const int row_lo = blockIdx.y * (kNormUnroll * per_token);                 // this CTA's rows of each token
+    const int row_n = min(rows - row_lo, kNormUnroll * per_token);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kWarps);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    for (int i = threadIdx.x; i < 2 * D; i += kNormThreads + 32)
+        weights[i] = to_float(static_cast<const TIN*>(i < D ? p.q_weight : p.k_weight)[i % D]);
+    __syncthreads();
+
+    // =========================== producer warp: lane i brings token i of a set
+    if (threadIdx.x >= kNormThreads) {
+        const int lane = threadIdx.x & 31;
+        // this CTA's rows are up to three runs of memory: of q, of k and of v
+        const int nq = max(0, min(Hq, row_lo + row_n) - row_lo);
+        const int k_lo = max(0, row_lo - Hq), nk = max(0, min(Hkv, row_lo + row_n - Hq) - k_lo);
+        const int v_lo = max(0, row_lo - Hq - Hkv), nv = row_n - nq - nk;
+        bool aborted = false;
+        int k = 0;
+        for (int base = blockIdx.x * tokens; base < p.num_tokens && !aborted; base += stride, ++k) {
+            const int st = k % S;
+            const int n = min(tokens, p.num_tokens - base);
+            if (lane == 0) {
+                if (*abort_flag || (k >= S && !mbar_wait_bounded(&empty[st], ((k / S) - 1) & 1)))
+                    aborted = true;
+                else
+                    mbar_arrive_expect_tx(&full[st], n * row_n * kRowBytes);
+            }
+            aborted = __shfl_sync(kFullMask, aborted ? 1 : 0, 0) != 0;
+            __syncwarp();
+            if (!aborted && lane < n) {
+                const long long t = base + lane;
+                uint8_t* dst = smem + st * p.stage_bytes + lane * (row_n * kRowBytes);
+                if (nq)
+                    bulk_copy_g2s(dst, static_cast<const TIN*>(p.q) + t * p.q_stride + (long long)row_lo * D,
+                                  nq * kRowBytes, &full[st]);
+                if (nk)
+                    bulk_copy_g2s(dst + nq * kRowBytes, static_cast<const TIN*>(p.k) + t * p.k_stride + (long long)k_lo * D,
+                                  nk * kRowBytes, &full[st]);
+                if (nv)
+                    bulk_copy_g2s(dst + (nq + nk) * kRowBytes,
+                                  static_cast<const TIN*>(p.v) + t * p.v_stride + (long long)v_lo * D, nv * kRowBytes,
+                                  &full[st]);
+            }
+        }
+        if (aborted && lane == 0) {      // a wait gave up: the copies under way end before the CTA does
+            *abort_flag = 1;
+            if (p.err)
+                atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+            for (int i = max(0, k - 1 - S); i < k - 1; ++i)
+                (void)mbar_wait_bounded(&full[i % S], (i / S) & 1);
+        }
+        return;
+    }
+
+    // =========================== the other warps
+    const int lane = threadIdx.x % LPR, group = threadIdx.x / LPR;
+    const int first = group % per_token, set_token = group / per_token;
+    const bool report = lane == 0 && first == 0 && blockIdx.y == 0 && p.err != nullptr;
 
     // this lane's two chunks of a row
-    const int half = p.rotary / 2;
-    const bool rotated = 8 * lane < p.rotary;
-    const bool split = rotated && !p.interleaved;
+    const int half = WHOLE ? D / 2 : p.rotary / 2;
+    const bool rotated = WHOLE || 8 * lane < p.rotary;
+    const bool split = WHOLE || (rotated && !p.interleaved);
     const int d0 = split ? 4 * lane : 8 * lane;
-    const int d1 = split ? half + 4 * lane : 8 * lane + 4;
+    const int d1 = WHOLE ? d0 + D / 2 : split ? half + 4 * lane : 8 * lane + 4;
+    const int apart = WHOLE ? D / 2 : d1 - d0;
 
-    const TIN* qrow = static_cast<const TIN*>(p.q) + t * p.q_stride;
-    const TIN* krow = static_cast<const TIN*>(p.k) + t * p.k_stride;
-    const TIN* vrow = static_cast<const TIN*>(p.v) + t * p.v_stride;
-    Raw4<TIN> a[kNormUnroll], b[kNormUnroll];
-    auto load_rows = [&](int r0) {
+    // this thread's rows, the same ones of every token it takes, and where they go but for the token
+    enum Kind { kQ, kK, kV, kNone };
+    int kind[kNormUnroll];
+    void* dst[kNormUnroll];
+    const long long head_rows = (long long)p.block_size * D;   // elements between a block's KV heads
 #pragma unroll
-        for (int u = 0; u < kNormUnroll; ++u) {
-            const int r = r0 + u * per_token;
-            if (real && r < rows) {
-                const TIN* x = r < Hq ? qrow + r * D : r < Hq + Hkv ? krow + (r - Hq) * D : vrow + (r - Hq - Hkv) * D;
-                a[u].load(x + d0);
-                b[u].load(x + d1);
-            } else {
-                a[u].clear();
-                b[u].clear();
-            }
-        }
-    };
-    load_rows(first);    // before anything that waits for a load: the rows are what takes time
-
-    float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-    bool live = real;
-    long long slot = -1;
-    if (real) {
-        const long long pos = __ldg(p.positions + t);
-        if (p.slots)
-            slot = __ldg(p.slots + t);
-        if (pos < 0 || pos >= p.num_positions) {
-            if (lane == 0 && first == 0 && p.err)
-                atomicOr(p.err, PKV_DEVERR_POSITION);
-            live = false;
+    for (int u = 0; u < kNormUnroll; ++u) {
+        const int r = row_lo + first + u * per_token;
+        if (r < Hq) {
+            kind[u] = kQ;
+            dst[u] = static_cast<TIN*>(p.q_out) + (long long)r * D + d0;
+        } else if (r < Hq + Hkv) {
+            kind[u] = kK;
+            dst[u] = CACHED ? static_cast<void*>(static_cast<TC*>(p.k_cache) + (r - Hq) * head_rows + d0)
+                            : static_cast<void*>(static_cast<TIN*>(p.k_out) + (long long)(r - Hq) * D + d0);
+        } else if (r < rows) {
+            kind[u] = kV;
+            dst[u] = static_cast<TC*>(p.v_cache) + (r - Hq - Hkv) * head_rows + d0;
         } else {
-            if (rotated) {
-                const float* cs = p.cos_sin + pos * p.rotary;
-                c = __ldg(reinterpret_cast<const float4*>(cs + 4 * lane));
-                s = __ldg(reinterpret_cast<const float4*>(cs + half + 4 * lane));
-            }
-            if (slot >= p.capacity) {
-                if (lane == 0 && first == 0 && p.err)
-                    atomicOr(p.err, PKV_DEVERR_SLOT);
-                slot = -1;
-            }
+            kind[u] = kNone;
+            dst[u] = nullptr;
         }
     }
-    Raw4<TIN> qw0, qw1, kw0, kw1;
-    qw0.load(static_cast<const TIN*>(p.q_weight) + d0);
-    qw1.load(static_cast<const TIN*>(p.q_weight) + d1);
-    kw0.load(static_cast<const TIN*>(p.k_weight) + d0);
-    kw1.load(static_cast<const TIN*>(p.k_weight) + d1);
-    // offset of this token's row of KV head 0 in the caches; heads lie block_size rows apart
-    const long long head_rows = (long long)p.block_size * D;
-    const long long blk = slot >= 0 ? slot / p.block_size : 0;
-    const long long at = blk * Hkv * head_rows + (slot >= 0 ? slot - blk * p.block_size : 0) * D;
+    const TIN* staged = reinterpret_cast<const TIN*>(smem) + (set_token * row_n + first) * D + d0;
 
-    for (int r0 = first;;) {
+    auto load_index = [&](int tok, long long& pos, long long& slot) {
+        pos = -1;
+        slot = -1;
+        if (tok < p.num_tokens) {
+            pos = __ldg(p.positions + tok);
+            if (CACHED)
+                slot = __ldg(p.slots + tok);
+        }
+    };
+    auto load_angles = [&](long long pos, float4& c, float4& s) {
+        c = make_float4(1.f, 1.f, 1.f, 1.f);
+        s = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (rotated && pos >= 0 && pos < p.num_positions) {
+            const float* cs = p.cos_sin + pos * p.rotary;
+            c = __ldg(reinterpret_cast<const float4*>(cs + 4 * lane));
+            s = __ldg(reinterpret_cast<const float4*>(cs + half + 4 * lane));
+        }
+    };
+    // the next token's cosines and sines and the position of the one after it are on their way while
+    // one is worked on (num_tokens and two strides fit 32 bits: the launcher bounds both)
+    int t = blockIdx.x * tokens + set_token;
+    float4 c, s, nc, ns;
+    long long pos, slot, npos, nslot, npos2, nslot2;
+    load_index(t, pos, slot);
+    load_index(t + stride, npos, nslot);
+    load_angles(pos, c, s);
+
+    int k = 0;
+    for (int base = blockIdx.x * tokens; base < p.num_tokens; base += stride, t += stride, ++k) {
+        const bool real = t < p.num_tokens;
+        load_index(t + 2 * stride, npos2, nslot2);
+        load_angles(npos, nc, ns);
+
+        const bool live = real && pos >= 0 && pos < p.num_positions;
+        if (real && !live && report)
+            atomicOr(p.err, PKV_DEVERR_POSITION);
+        if (CACHED && live && slot >= p.capacity) {
+            if (report)
+                atomicOr(p.err, PKV_DEVERR_SLOT);
+            slot = -1;
+        }
+        // element offsets of this token's outputs and of its row in a block's KV head 0
+        const long long q_at = (long long)t * Hq * D, k_at = (long long)t * Hkv * D;
+        long long cache_at = 0;
+        if (CACHED && slot >= 0) {       // (block sizes are powers of two)
+            const long long blk = slot >> p.block_shift;
+            cache_at = blk * Hkv * head_rows + (slot & (p.block_size - 1)) * D;
+        }
+        const Pairs cp = pairs(c), sp = pairs(s), np = pairs(make_float4(-s.x, -s.y, -s.z, -s.w));
+
+        const int st = k % S;
+        const bool ok = !*abort_flag && mbar_wait_bounded(&full[st], (k / S) & 1);
+        if (!__all_sync(kFullMask, ok)) {
+            if ((threadIdx.x & 31) == 0) {
+                *abort_flag = 1;
+                if (p.err)
+                    atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+            }
+            break;
+        }
+        const TIN* x0 = staged + st * (p.stage_bytes / (int)sizeof(TIN));
 #pragma unroll
         for (int u = 0; u < kNormUnroll; ++u) {
-            const int r = r0 + u * per_token;
-            const float4 xa = a[u].get(), xb = b[u].get();
-            float ss = xa.x * xa.x + xa.y * xa.y + xa.z * xa.z + xa.w * xa.w + xb.x * xb.x + xb.y * xb.y +
-                       xb.z * xb.z + xb.w * xb.w;
+            Raw4<TIN> a, b;
+            a.clear();
+            b.clear();
+            if (real && kind[u] != kNone) {
+                a.load(x0 + u * per_token * D);
+                b.load(x0 + u * per_token * D + apart);
+            }
+            const float4 fa = a.get(), fb = b.get();
+            const Pairs xa = pairs(fa), xb = pairs(fb);
+            const Pairs sq = plus_times(xa, xa, times(xb, xb));
+            const float4 sum4 = singles(sq);
+            float ss = (sum4.x + sum4.y) + (sum4.z + sum4.w);
 #pragma unroll
             for (int o = 1; o < LPR; o <<= 1)
                 ss += __shfl_xor_sync(kFullMask, ss, o);
-            if (!live || r >= rows)
+            if (!live || kind[u] == kNone)
                 continue;
-            if (r >= Hq + Hkv) {   // a V row: only appended
+            if (CACHED && kind[u] == kV) {   // only appended
                 if (slot >= 0) {
-                    TC* dst = static_cast<TC*>(p.v_cache) + at + (r - Hq - Hkv) * head_rows;
-                    cache4<TC, FMT>(dst + d0, xa, p.v_scale);
-                    cache4<TC, FMT>(dst + d1, xb, p.v_scale);
+                    TC* at = static_cast<TC*>(dst[u]) + cache_at;
+                    if constexpr (std::is_same<TIN, TC>::value) {   // the bits as they are
+                        a.store(at);
+                        b.store(at + apart);
+                    } else {
+                        cache4<TC, FMT>(at, fa, p.v_scale);
+                        cache4<TC, FMT>(at + apart, fb, p.v_scale);
+                    }
                 }
                 continue;
             }
             const float inv = rsqrtf(ss * (1.0f / D) + p.eps);
-            const bool is_q = r < Hq;
-            const float4 i4 = make_float4(inv, inv, inv, inv);
-            const float4 x = times(times(xa, i4), is_q ? qw0.get() : kw0.get());
-            const float4 y = times(times(xb, i4), is_q ? qw1.get() : kw1.get());
-            float4 u0 = x, u1 = y;
-            if (split) {
-                u0 = make_float4(x.x * c.x - y.x * s.x, x.y * c.y - y.y * s.y, x.z * c.z - y.z * s.z,
-                                 x.w * c.w - y.w * s.w);
-                u1 = make_float4(y.x * c.x + x.x * s.x, y.y * c.y + x.y * s.y, y.z * c.z + x.z * s.z,
-                                 y.w * c.w + x.w * s.w);
-            } else if (rotated) {
-                u0 = make_float4(x.x * c.x - x.y * s.x, x.y * c.x + x.x * s.x, x.z * c.y - x.w * s.y,
-                                 x.w * c.y + x.z * s.y);
-                u1 = make_float4(y.x * c.z - y.y * s.z, y.y * c.z + y.x * s.z, y.z * c.w - y.w * s.w,
-                                 y.w * c.w + y.z * s.w);
+            const float* w = weights + kind[u] * D + d0;
+            const Pairs i4 = pairs(make_float4(inv, inv, inv, inv));
+            const Pairs x = times(xa, times(i4, pairs(*reinterpret_cast<const float4*>(w))));
+            const Pairs y = times(xb, times(i4, pairs(*reinterpret_cast<const float4*>(w + apart))));
+            float4 u0, u1;
+            if (!rotated) {
+                u0 = singles(x);
+                u1 = singles(y);
+            } else if (split) {
+                u0 = singles(plus_times(x, cp, times(y, np)));
+                u1 = singles(plus_times(y, cp, times(x, sp)));
+            } else {
+                const float4 e = singles(x), f = singles(y);
+                u0 = make_float4(e.x * c.x - e.y * s.x, e.y * c.x + e.x * s.x, e.z * c.y - e.w * s.y,
+                                 e.w * c.y + e.z * s.y);
+                u1 = make_float4(f.x * c.z - f.y * s.z, f.y * c.z + f.x * s.z, f.z * c.w - f.w * s.w,
+                                 f.w * c.w + f.z * s.w);
             }
-            if (is_q || !p.slots) {
-                TIN* dst = is_q ? static_cast<TIN*>(p.q_out) + (t * Hq + r) * D
-                                : static_cast<TIN*>(p.k_out) + (t * Hkv + (r - Hq)) * D;
-                store4(dst + d0, u0);
-                store4(dst + d1, u1);
+            if (!CACHED || kind[u] == kQ) {
+                TIN* at = static_cast<TIN*>(dst[u]) + (kind[u] == kQ ? q_at : k_at);
+                store4(at, u0);
+                store4(at + apart, u1);
             } else if (slot >= 0) {
-                TC* dst = static_cast<TC*>(p.k_cache) + at + (r - Hq) * head_rows;
-                cache4<TC, FMT>(dst + d0, u0, p.k_scale);
-                cache4<TC, FMT>(dst + d1, u1, p.k_scale);
+                TC* at = static_cast<TC*>(dst[u]) + cache_at;
+                cache4<TC, FMT>(at, u0, p.k_scale);
+                cache4<TC, FMT>(at + apart, u1, p.k_scale);
             }
         }
-        r0 += kNormUnroll * per_token;
-        if (r0 - first >= rows)
-            break;
-        load_rows(r0);
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0)
+            mbar_arrive(&empty[st]);
+        c = nc;
+        s = ns;
+        pos = npos;
+        slot = nslot;
+        npos = npos2;
+        nslot = nslot2;
     }
+}
+
+template <class TIN, class TC, int D, __nv_fp8_interpretation_t FMT, bool WHOLE, bool CACHED>
+int launch_norm_rope_kernel(const NormRopeArgs& p, dim3 grid, cudaStream_t stream)
+{
+    auto kern = norm_rope_kernel<TIN, TC, D, FMT, WHOLE, CACHED>;
+    const size_t smem = NormSmem<TIN, D>::bytes(p.stages, p.stage_bytes);
+    if (!ensure_smem_attribute((const void*)kern, NormSmem<TIN, D>::bytes(1, NormSmem<TIN, D>::kBudget)))
+        return PKV_ERR_LAUNCH;
+    kern<<<grid, kNormThreads + 32, smem, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_LAUNCH;
 }
 
 template <class TIN, class TC, int D, __nv_fp8_interpretation_t FMT = __NV_E4M3>
 int launch_norm_rope(NormRopeArgs p, cudaStream_t stream)
 {
     constexpr int kGroups = kNormThreads / (D / 8);
-    const int rows = p.num_heads + p.num_kv_heads + (p.v ? p.num_kv_heads : 0);
+    const bool cached = p.slots != nullptr;
+    const int rows = p.num_heads + p.num_kv_heads + (cached ? p.num_kv_heads : 0);
     int per = 1;
     while (per < kGroups && per < rows)
         per *= 2;
     p.groups_per_token = per;
     const int tokens_per_cta = kGroups / per;
-    const int grid = (p.num_tokens + tokens_per_cta - 1) / tokens_per_cta;
-    norm_rope_kernel<TIN, TC, D, FMT><<<grid, kNormThreads, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_LAUNCH;
+    const int passes = (rows + kNormUnroll * per - 1) / (kNormUnroll * per);
+    const int rows_per_pass = rows < kNormUnroll * per ? rows : kNormUnroll * per;
+    p.stage_bytes = tokens_per_cta * rows_per_pass * D * (int)sizeof(TIN);   // at most 16 KB (fp32: 32 KB)
+    p.stages = NormSmem<TIN, D>::stages(p.stage_bytes);
+    // three CTAs an SM (fp32 rows: two), each taking every so many tokens; with few tokens a CTA has one
+    int grid = (p.num_tokens + tokens_per_cta - 1) / tokens_per_cta;
+    const int most = ((sizeof(TIN) == 2 ? 3 : 2) * 148 + passes - 1) / passes;
+    if (grid > most)
+        grid = most;
+    const bool whole = p.rotary == D && !p.interleaved;
+    const dim3 g(grid, passes);
+    if (cached)
+        return whole ? launch_norm_rope_kernel<TIN, TC, D, FMT, true, true>(p, g, stream)
+                     : launch_norm_rope_kernel<TIN, TC, D, FMT, false, true>(p, g, stream);
+    if constexpr (std::is_same<TIN, TC>::value)
+        return whole ? launch_norm_rope_kernel<TIN, TC, D, FMT, true, false>(p, g, stream)
+                     : launch_norm_rope_kernel<TIN, TC, D, FMT, false, false>(p, g, stream);
+    return PKV_ERR_DTYPE;
 }
 
 template <class TIN, int D>
@@ -285,7 +490,8 @@ bool rows_clash(const void* out, long long out_row, const void* in, long long in
 int norm_rope_impl(NormRopeArgs p, int head_dim, int num_blocks, int in_dtype, int kv_dtype, bool cached,
                    cudaStream_t stream)
 {
-    if (p.num_tokens < 0 || p.num_heads <= 0 || p.num_kv_heads <= 0 || (head_dim != 64 && head_dim != 128) ||
+    if (p.num_tokens < 0 || p.num_tokens > (1 << 30) || p.num_heads <= 0 || p.num_kv_heads <= 0 ||
+        (long long)p.num_heads + 2ll * p.num_kv_heads > 65536 || (head_dim != 64 && head_dim != 128) ||
         p.rotary < 0 || p.rotary > head_dim || p.rotary % 8 != 0 || p.num_positions < 0 || !(p.eps >= 0.0f))
         return PKV_ERR_SHAPE;
     if (in_dtype != PKV_F32 && in_dtype != PKV_BF16)
@@ -324,6 +530,7 @@ int norm_rope_impl(NormRopeArgs p, int head_dim, int num_blocks, int in_dtype, i
                     overlap(p.k_out, T * k_row * elt, p.q_out, T * q_row * elt)))
         return PKV_ERR_SHAPE;
     p.capacity = (long long)num_blocks * p.block_size;
+    p.block_shift = p.block_size == 8 ? 3 : p.block_size == 16 ? 4 : 5;
     const int kv = cached ? kv_dtype : in_dtype;
     if (in_dtype == PKV_F32)
         return head_dim == 128 ? norm_rope_by_cache<float, 128>(p, kv, stream)

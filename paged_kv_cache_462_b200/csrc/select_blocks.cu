@@ -183,7 +183,7 @@ __device__ __forceinline__ double exact_score(const __nv_bfloat16* q, const __nv
 }
 
 template <int D, int G>
-__global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const SelectArgs p)
+__global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const SelectArgs p)
 {
     constexpr int NC = D / 32;           // 16-byte pieces of one bound a lane holds
     extern __shared__ uint32_t smem_keys[];
@@ -224,68 +224,85 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
 
     // ---- scores of this CTA's blocks
     {
-        uint32_t qp[NC][4], qn[NC][4];   // q+ and q- of column g in the order of the bounds' pieces
+        uint32_t qw[NC][4];              // column g of q in the order of the bounds' pieces
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             uint4 u = make_uint4(0u, 0u, 0u, 0u);
             if (g < G)
                 u = __ldg(reinterpret_cast<const uint4*>(q + (long long)g * D) + 4 * c + t);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-            const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
-                const __nv_bfloat162 a = __hmax2_nan(x, zero), b = __hmin2_nan(x, zero);
-                qp[c][i] = *reinterpret_cast<const uint32_t*>(&a);
-                qn[c][i] = *reinterpret_cast<const uint32_t*>(&b);
-            }
+            qw[c][0] = u.x;
+            qw[c][1] = u.y;
+            qw[c][2] = u.z;
+            qw[c][3] = u.w;
         }
+        // q+ and q- of a pair (kept as one to hold fewer registers)
+        auto plus = [](uint32_t x) -> uint32_t {
+            const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&x), __floats2bfloat162_rn(0.f, 0.f));
+            return *reinterpret_cast<const uint32_t*>(&r);
+        };
+        auto minus = [](uint32_t x) -> uint32_t {
+            const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<const __nv_bfloat162*>(&x), __floats2bfloat162_rn(0.f, 0.f));
+            return *reinterpret_cast<const uint32_t*>(&r);
+        };
         float mag = 0.f;
+        // Bounds are always on their way: as soon as a tile's maxima are used the next tile's take
+        // their registers, then the minima; the table's entries that lead to them come another tile
+        // ahead.
+        auto entry = [&](int tile, int r) -> int {
+            const int j = chunk * per_cta + tile * kSelTile + warp * 16 + g + 8 * r;
+            return tile < p.tiles && j < nb ? __ldg(table + j) : -1;
+        };
+        auto tile_of = [&](int phys) -> int {   // (block, KV head), or -1
+            return phys >= 0 && phys < p.num_blocks ? phys * p.num_kv_heads + h : -1;
+        };
+        uint4 hi[2][NC], lo[2][NC];
+        auto fetch = [&](uint4 (&x)[2][NC], int tile0, int tile1, int from) {
+            const uint4* base = reinterpret_cast<const uint4*>(p.bounds) + from + t;
+            const uint4 *r0 = base + tile0 * (long long)(D / 4), *r1 = base + tile1 * (long long)(D / 4);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                x[0][c] = tile0 >= 0 ? __ldg(r0 + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
+                x[1][c] = tile1 >= 0 ? __ldg(r1 + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        };
+        int row0 = tile_of(entry(0, 0)), row1 = tile_of(entry(0, 1));
+        fetch(hi, row0, row1, 0);
+        fetch(lo, row0, row1, D / 8);
+        int next0 = entry(1, 0), next1 = entry(1, 1);
         for (int tile = 0; tile < p.tiles; ++tile) {
             const int first = chunk * per_cta + tile * kSelTile + warp * 16;
             if (first >= nb)
                 break;
-            uint4 hi[2][NC], lo[2][NC];
-            bool ok[2];
+            const bool ok[2] = {row0 >= 0, row1 >= 0};
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int j = first + g + 8 * r;
-                int phys = -1;
-                if (j < nb) {
-                    phys = __ldg(table + j);
-                    if (phys < 0 || phys >= p.num_blocks) {
-                        if (t == 0 && h == 0)
-                            atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
-                        phys = -1;
-                    }
-                }
-                ok[r] = phys >= 0;
-                const uint4* row = reinterpret_cast<const uint4*>(
-                    p.bounds + ((long long)phys * p.num_kv_heads + h) * (2 * D));
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    hi[r][c] = ok[r] ? __ldg(row + 4 * c + t) : make_uint4(0u, 0u, 0u, 0u);
-                    lo[r][c] = ok[r] ? __ldg(row + D / 8 + 4 * c + t) : make_uint4(0u, 0u, 0u, 0u);
-                }
-            }
-            // sc: the scores; ab and an: the sums of |q+ kmax| and of -|q- kmin|
-            float sc[4] = {0.f, 0.f, 0.f, 0.f}, ab[4] = {0.f, 0.f, 0.f, 0.f}, an[4] = {0.f, 0.f, 0.f, 0.f};
-            auto product = [&](const uint4& x, const uint4& y, const uint32_t (&b)[4], float (&size)[4]) {
+            for (int r = 0; r < 2; ++r)
+                if (!ok[r] && first + g + 8 * r < nb && t == 0 && h == 0)
+                    atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
+            row0 = tile_of(next0);
+            row1 = tile_of(next1);
+            next0 = entry(tile + 2, 0);
+            next1 = entry(tile + 2, 1);
+            // sc: the scores; ab: the sums of |q+ kmax| and |q- kmin|
+            float sc[4] = {0.f, 0.f, 0.f, 0.f}, ab[4] = {0.f, 0.f, 0.f, 0.f};
+            auto product = [&](const uint4& x, const uint4& y, uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3) {
                 constexpr uint32_t M = 0x7fff7fffu;
                 float c[4];
-                mma_bf16_zero(c, x.x, y.x, x.y, y.y, b[0], b[1]);
-                mma_bf16(c, x.z, y.z, x.w, y.w, b[2], b[3]);
+                mma_bf16_zero(c, x.x, y.x, x.y, y.y, b0, b1);
+                mma_bf16(c, x.z, y.z, x.w, y.w, b2, b3);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     sc[i] += c[i];
-                mma_bf16(size, x.x & M, y.x & M, x.y & M, y.y & M, b[0], b[1]);
-                mma_bf16(size, x.z & M, y.z & M, x.w & M, y.w & M, b[2], b[3]);
+                mma_bf16(ab, x.x & M, y.x & M, x.y & M, y.y & M, b0 & M, b1 & M);
+                mma_bf16(ab, x.z & M, y.z & M, x.w & M, y.w & M, b2 & M, b3 & M);
             };
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                product(hi[0][c], hi[1][c], qp[c], ab);
-                product(lo[0][c], lo[1][c], qn[c], an);
-            }
+            for (int c = 0; c < NC; ++c)
+                product(hi[0][c], hi[1][c], plus(qw[c][0]), plus(qw[c][1]), plus(qw[c][2]), plus(qw[c][3]));
+            fetch(hi, row0, row1, 0);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                product(lo[0][c], lo[1][c], minus(qw[c][0]), minus(qw[c][1]), minus(qw[c][2]), minus(qw[c][3]));
+            fetch(lo, row0, row1, D / 8);
             // rows first + g (sc 0, 1) and first + g + 8 (sc 2, 3), columns 2t and 2t + 1
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -295,7 +312,7 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
                     if (2 * t + i < G) {
                         const float x = sc[2 * r + i];
                         best = fmaxf(best, finite(x) ? x : INFINITY);
-                        a = fmaxf(a, ab[2 * r + i] - an[2 * r + i]);
+                        a = fmaxf(a, ab[2 * r + i]);
                     }
                 }
 #pragma unroll
@@ -618,7 +635,7 @@ PKV_API int select_blocks(int32_t* selected, const void* q, const void* key_boun
     if (!select_sizes_ok(num_seqs, num_kv_heads, max_blocks_per_seq) || num_heads <= 0 ||
         num_heads % num_kv_heads != 0 || (head_dim != 64 && head_dim != 128) ||
         (block_size != 8 && block_size != 16 && block_size != 32) || num_blocks <= 0 ||
-        (long long)max_blocks_per_seq * block_size >= (1ll << 31) || num_selected < 1 || num_sink_blocks < 0 ||
+        (long long)num_blocks * num_kv_heads >= (1ll << 31) || (long long)max_blocks_per_seq * block_size >= (1ll << 31) || num_selected < 1 || num_sink_blocks < 0 ||
         num_recent_blocks < 0 || (long long)num_sink_blocks + num_recent_blocks > num_selected ||
         (long long)num_seqs * num_kv_heads * num_selected >= (1ll << 31))
         return PKV_ERR_SHAPE;
