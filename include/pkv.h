@@ -460,7 +460,7 @@ PKV_API int paged_attention_decode_block_scales(void* out, const void* q, const 
  * finite ranks first, one with a bad block id (PKV_DEVERR_BLOCK_ID) last. q is bf16. The
  * workspace (pkv_select_workspace_size bytes) starts zeroed (pkv_workspace_init) and holds the
  * error word; one can serve calls of any sizes it is large enough for, but calls that share one
- * must not overlap on the GPU. num_seqs * num_kv_heads <= 2^18; groups as everywhere.
+ * must not overlap on the GPU. Two launches, in order on `stream`.
  *
  * paged_attention_decode_sparse attends, for KV head h of sequence s, the tokens of the listed
  * blocks only. Of a list the first min(num_selected, ceil(seq_lens[s] / block_size)) entries are

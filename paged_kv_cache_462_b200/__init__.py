@@ -708,7 +708,7 @@ def select_blocks(selected, q, key_bounds, block_tables, seq_lens, block_size, n
     if S2 != S:
         raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
     if workspace is None:
-        workspace = _op_workspace("select", select_workspace_size(S, Hkv, max(1, MB)), 256 + (4 << 18), dev, stream)
+        workspace = _op_workspace("select", select_workspace_size(S, Hkv, max(1, MB)), 256, dev, stream)
     st = load_library().select_blocks(
         _cuda("selected", selected, dev), _cuda("q", q, dev), _cuda("key_bounds", key_bounds, dev), bt, sl, S, Hq, Hkv,
         D, int(block_size), MB, NB, selected.shape[2], int(num_sink_blocks), int(num_recent_blocks),

@@ -21,10 +21,11 @@
 // scored again in fp64, where products of bf16 numbers and their sums are exact but for terms
 // 2^-30 apart. A block whose score is not finite ranks first.
 //
-// One launch: a CTA scores some blocks of one (sequence, KV head); the last of a stream's CTAs to
-// arrive (a counter in the workspace, left at zero) selects among them.
+// Two launches. The first streams the bounds: a block's bounds of neighbouring KV heads are one run of
+// memory, so a producer warp brings 16 blocks (or a few times 16) of up to four heads at a time into
+// a ring of shared-memory stages by bulk copies, and a warp per head and 16 blocks turns them into
+// scores. The second, queued behind it as a dependent launch, selects: a CTA per stream.
 #include <cstdint>
-#include <cstdlib>
 
 #include "device.cuh"
 #include "pkv_internal.h"
@@ -33,15 +34,15 @@ namespace pkv {
 
 namespace {
 
+constexpr int kScoreWarps = 4;                // consumer warps, each a KV head's 16 blocks of a stage
+constexpr int kScoreThreads = (kScoreWarps + 1) * 32;
+constexpr int kScoreStages = 3;
+constexpr int kRowPad = 64;                   // bytes behind a block's run: neighbouring rows meet other banks
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelTile = 16 * kSelWarps;      // blocks a CTA scores at a time
 constexpr int kSelSmemKeys = 8192;            // streams of up to this many blocks are selected in shared memory
 constexpr float kSelError = 7.62939453125e-06f;   // 2^-17
 constexpr uint32_t kChosen = 0xffffffffu;
-// (sequence, KV head) pairs of a call; their counters have this room whatever the call's sizes, so
-// that calls of other sizes, whose scores lie behind it, never write there
-constexpr long long kSelMaxStreams = 1ll << 18;
 
 struct SelectArgs {
     int32_t* selected;            // [num_seqs][num_kv_heads][keep]
@@ -50,14 +51,24 @@ struct SelectArgs {
     const int32_t* block_tables;
     const int32_t* seq_lens;
     int32_t* err;
-    int32_t* arrived;             // [streams], zero between calls
-    float* magnitude;             // [streams][chunks]: largest A of a chunk
+    float* magnitude;             // [streams][parts]: largest A of a warp's share
     float* scores;                // [streams][max_blocks]
     int32_t* near_list;           // [streams][max_blocks]: blocks near the border
     double* near_score;           // [streams][max_blocks]
     int num_heads, num_kv_heads, max_blocks, num_blocks, block_size;
-    int keep, sink, recent, chunks, tiles;   // tiles: of kSelTile blocks, per CTA
+    int keep, sink, recent;
+    int heads, head_groups;       // KV heads a scoring CTA takes (the last group may have fewer)
+    int tiles;                    // runs of 16 blocks in a stage
+    int rounds, chunks;           // stages a scoring CTA takes, such CTAs for the widest sequence
+    int parts;                    // chunks * tiles
 };
+
+// Tokens of sequence s as the table can hold them.
+__device__ __forceinline__ int held_tokens(const SelectArgs& p, int s)
+{
+    const int L = __ldg(p.seq_lens + s), capacity = p.max_blocks * p.block_size;
+    return L < 0 ? 0 : min(L, capacity);
+}
 
 __device__ __forceinline__ void mma_bf16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1)
@@ -183,9 +194,199 @@ __device__ __forceinline__ double exact_score(const __nv_bfloat16* q, const __nv
 }
 
 template <int D, int G>
-__global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const SelectArgs p)
+__global__ void __launch_bounds__(kScoreThreads, 2) score_blocks_kernel(const SelectArgs p)
 {
-    constexpr int NC = D / 32;           // 16-byte pieces of one bound a lane holds
+    constexpr int NC = D / 32;           // 16-byte pieces of one bound a lane takes
+    constexpr int kTileBytes = 4 * D;    // one (block, KV head): maxima and minima
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int row_bytes = p.heads * kTileBytes + kRowPad;      // a block's run in a stage
+    const int stage_blocks = 16 * p.tiles;
+    const int stage_bytes = stage_blocks * row_bytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kScoreStages * stage_bytes);
+    uint64_t* empty = full + kScoreStages;
+    int* held = reinterpret_cast<int*>(empty + kScoreStages);  // [stages][stage_blocks]: a good block id
+    volatile int* abort_flag = held + kScoreStages * 16 * kScoreWarps;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int chunk = blockIdx.x % p.chunks, hg = blockIdx.x / p.chunks % p.head_groups;
+    const int s = blockIdx.x / p.chunks / p.head_groups;
+    const int h0 = hg * p.heads, heads = min(p.heads, p.num_kv_heads - h0);
+    const int L = __ldg(p.seq_lens + s);
+    if ((L < 0 || L > p.max_blocks * p.block_size) && chunk == 0 && hg == 0 && tid == 0)
+        atomicOr(p.err, PKV_DEVERR_SEQ_LEN);
+    const int nb = (held_tokens(p, s) + p.block_size - 1) / p.block_size;
+    const int begin = chunk * p.rounds * stage_blocks;
+    if (nb <= p.keep || begin >= nb)     // nothing to choose, or not here
+        return;
+    const int end = min(nb, begin + p.rounds * stage_blocks);
+    const int active = heads * p.tiles;  // warps with work
+
+    if (tid == 0) {
+        for (int i = 0; i < kScoreStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], active);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    const int32_t* table = p.block_tables + (long long)s * p.max_blocks;
+
+    if (warp == kScoreWarps) {           // the producer: lanes share a stage's blocks
+        auto entry = [&](int j) -> int { return j < end ? __ldg(table + j) : -1; };
+        int next[2] = {entry(begin + lane), entry(begin + 32 + lane)};   // a stage has at most 64 blocks
+        bool aborted = false;
+        int k = 0;
+        for (int base = begin; base < end && !aborted; base += stage_blocks, ++k) {
+            const int st = k % kScoreStages, n = min(stage_blocks, end - base);
+            const int phys[2] = {next[0], next[1]};
+            next[0] = entry(base + stage_blocks + lane);
+            next[1] = entry(base + stage_blocks + 32 + lane);
+            bool ok[2];
+            int copies = 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool mine = lane + 32 * i < n;
+                ok[i] = mine && phys[i] >= 0 && phys[i] < p.num_blocks;
+                if (mine && !ok[i] && hg == 0)
+                    atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
+                copies += __popc(__ballot_sync(kFullMask, ok[i]));
+            }
+            if (lane == 0 && (*abort_flag || (k >= kScoreStages &&
+                                              !mbar_wait_bounded(&empty[st], ((k / kScoreStages) - 1) & 1))))
+                aborted = true;
+            aborted = __shfl_sync(kFullMask, aborted ? 1 : 0, 0) != 0;
+            if (aborted)
+                break;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (lane + 32 * i < stage_blocks)
+                    held[st * stage_blocks + lane + 32 * i] = ok[i];
+            __syncwarp();                // the entries, before the arrival that publishes them
+            if (lane == 0) {
+                if (copies)
+                    mbar_arrive_expect_tx(&full[st], copies * heads * kTileBytes);
+                else
+                    mbar_arrive(&full[st]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (ok[i])
+                    bulk_copy_g2s(smem + st * stage_bytes + (lane + 32 * i) * row_bytes,
+                                  p.bounds + ((long long)phys[i] * p.num_kv_heads + h0) * (2 * D),
+                                  heads * kTileBytes, &full[st]);
+        }
+        if (aborted && lane == 0) {      // a wait gave up: the copies under way end before the CTA does
+            *abort_flag = 1;
+            atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+            for (int i = max(0, k - kScoreStages); i < k; ++i)
+                (void)mbar_wait_bounded(&full[i % kScoreStages], (i / kScoreStages) & 1);
+        }
+        return;
+    }
+    if (warp >= active)
+        return;
+
+    // ---- a consumer: KV head h0 + warp % heads, run warp / heads of each stage
+    const int hw = warp % heads, tile = warp / heads, h = h0 + hw;
+    const long long stream = (long long)s * p.num_kv_heads + h;
+    const __nv_bfloat16* q = p.q + ((long long)s * p.num_heads + (long long)h * G) * D;
+    float* scores = p.scores + stream * p.max_blocks;
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t qp[NC][4], qn[NC][4];       // q+ and q- of column g in the order of the bounds' pieces
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        if (g < G)
+            u = __ldg(reinterpret_cast<const uint4*>(q + (long long)g * D) + 4 * c + t);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+            const __nv_bfloat162 a = __hmax2_nan(x, zero), b = __hmin2_nan(x, zero);
+            qp[c][i] = *reinterpret_cast<const uint32_t*>(&a);
+            qn[c][i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+    }
+    float mag = 0.f;
+    int k = 0;
+    for (int base = begin; base < end; base += stage_blocks, ++k) {
+        const int st = k % kScoreStages;
+        const bool arrived = !*abort_flag && mbar_wait_bounded(&full[st], (k / kScoreStages) & 1);
+        if (!__all_sync(kFullMask, arrived)) {
+            if (lane == 0) {
+                *abort_flag = 1;
+                atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+            }
+            break;
+        }
+        const int first = base + tile * 16;
+        const int slot = st * stage_blocks + tile * 16 + g;
+        const bool ok[2] = {held[slot] != 0, held[slot + 8] != 0};   // rows g and g + 8
+        // sc: the scores; ab and an: the sums of |q+ kmax| and of -|q- kmin|. Rows without a block hold
+        // what was there before: nothing of theirs is used.
+        float sc[4] = {0.f, 0.f, 0.f, 0.f}, ab[4] = {0.f, 0.f, 0.f, 0.f}, an[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint8_t* at = smem + st * stage_bytes + (tile * 16 + g) * row_bytes + hw * kTileBytes + t * 16;
+        auto product = [&](const uint8_t* from, const uint32_t (&b)[4], float (&size)[4]) {
+            constexpr uint32_t M = 0x7fff7fffu;
+            const uint4 x = *reinterpret_cast<const uint4*>(from);
+            const uint4 y = *reinterpret_cast<const uint4*>(from + 8 * row_bytes);
+            float c[4];
+            mma_bf16_zero(c, x.x, y.x, x.y, y.y, b[0], b[1]);
+            mma_bf16(c, x.z, y.z, x.w, y.w, b[2], b[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                sc[i] += c[i];
+            mma_bf16(size, x.x & M, y.x & M, x.y & M, y.y & M, b[0], b[1]);
+            mma_bf16(size, x.z & M, y.z & M, x.w & M, y.w & M, b[2], b[3]);
+        };
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            product(at + 64 * c, qp[c], ab);
+            product(at + 64 * c + 2 * D, qn[c], an);
+        }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&empty[st]);
+        // rows first + g (sc 0, 1) and first + g + 8 (sc 2, 3), columns 2t and 2t + 1
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float best = -INFINITY, a = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (2 * t + i < G) {
+                    const float x = sc[2 * r + i];
+                    best = fmaxf(best, finite(x) ? x : INFINITY);
+                    a = fmaxf(a, ab[2 * r + i] - an[2 * r + i]);
+                }
+            }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                best = fmaxf(best, __shfl_xor_sync(kFullMask, best, o));
+                a = fmaxf(a, __shfl_xor_sync(kFullMask, a, o));
+            }
+            if (!ok[r])
+                best = -INFINITY;        // a bad block id: chosen last
+            else if (finite(best))
+                mag = fmaxf(mag, a);
+            const int j = first + g + 8 * r;
+            if (t == 0 && j < end)
+                scores[j] = best;
+        }
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+        mag = fmaxf(mag, __shfl_xor_sync(kFullMask, mag, o));
+    if (lane == 0)
+        p.magnitude[stream * p.parts + chunk * p.tiles + tile] = mag;
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const SelectArgs p)
+{
     extern __shared__ uint32_t smem_keys[];
     __shared__ int scratch[kSelWarps];
     __shared__ int2 scratch2[kSelWarps];
@@ -194,172 +395,28 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
     __shared__ int hist[256];
     __shared__ int bcast[3];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int stream = blockIdx.x / p.chunks, chunk = blockIdx.x - stream * p.chunks;
-    const int s = stream / p.num_kv_heads, h = stream - s * p.num_kv_heads;
+    const int stream = blockIdx.x, s = stream / p.num_kv_heads, h = stream - s * p.num_kv_heads;
     int32_t* out = p.selected + (long long)stream * p.keep;
-
-    int L = __ldg(p.seq_lens + s);
-    const int capacity = p.max_blocks * p.block_size;
-    if (L < 0 || L > capacity) {
-        if (chunk == 0 && h == 0 && tid == 0)
-            atomicOr(p.err, PKV_DEVERR_SEQ_LEN);
-        L = L < 0 ? 0 : capacity;
-    }
-    const int nb = (L + p.block_size - 1) / p.block_size;
+    const int nb = (held_tokens(p, s) + p.block_size - 1) / p.block_size;
+    // (the scoring grid may still run; the next call's waits for this one's end)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (nb <= p.keep) {                  // everything is kept
-        if (chunk == 0)
-            for (int i = tid; i < p.keep; i += kSelThreads)
-                out[i] = i < nb ? i : -1;
+        for (int i = tid; i < p.keep; i += kSelThreads)
+            out[i] = i < nb ? i : -1;
         return;
     }
-    const int per_cta = kSelTile * p.tiles;
-    const int active = (nb + per_cta - 1) / per_cta;
-    if (chunk >= active)
-        return;
-
     const __nv_bfloat16* q = p.q + ((long long)s * p.num_heads + (long long)h * G) * D;
     const int32_t* table = p.block_tables + (long long)s * p.max_blocks;
     float* scores = p.scores + (long long)stream * p.max_blocks;
-    const int g = lane >> 2, t = lane & 3;
+    const int stage_blocks = 16 * p.tiles;
+    const int active = (nb + p.rounds * stage_blocks - 1) / (p.rounds * stage_blocks) * p.tiles;
 
-    // ---- scores of this CTA's blocks
-    {
-        uint32_t qw[NC][4];              // column g of q in the order of the bounds' pieces
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            uint4 u = make_uint4(0u, 0u, 0u, 0u);
-            if (g < G)
-                u = __ldg(reinterpret_cast<const uint4*>(q + (long long)g * D) + 4 * c + t);
-            qw[c][0] = u.x;
-            qw[c][1] = u.y;
-            qw[c][2] = u.z;
-            qw[c][3] = u.w;
-        }
-        // q+ and q- of a pair (kept as one to hold fewer registers)
-        auto plus = [](uint32_t x) -> uint32_t {
-            const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&x), __floats2bfloat162_rn(0.f, 0.f));
-            return *reinterpret_cast<const uint32_t*>(&r);
-        };
-        auto minus = [](uint32_t x) -> uint32_t {
-            const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<const __nv_bfloat162*>(&x), __floats2bfloat162_rn(0.f, 0.f));
-            return *reinterpret_cast<const uint32_t*>(&r);
-        };
-        float mag = 0.f;
-        // Bounds are always on their way: as soon as a tile's maxima are used the next tile's take
-        // their registers, then the minima; the table's entries that lead to them come another tile
-        // ahead.
-        auto entry = [&](int tile, int r) -> int {
-            const int j = chunk * per_cta + tile * kSelTile + warp * 16 + g + 8 * r;
-            return tile < p.tiles && j < nb ? __ldg(table + j) : -1;
-        };
-        auto tile_of = [&](int phys) -> int {   // (block, KV head), or -1
-            return phys >= 0 && phys < p.num_blocks ? phys * p.num_kv_heads + h : -1;
-        };
-        uint4 hi[2][NC], lo[2][NC];
-        auto fetch = [&](uint4 (&x)[2][NC], int tile0, int tile1, int from) {
-            const uint4* base = reinterpret_cast<const uint4*>(p.bounds) + from + t;
-            const uint4 *r0 = base + tile0 * (long long)(D / 4), *r1 = base + tile1 * (long long)(D / 4);
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                x[0][c] = tile0 >= 0 ? __ldg(r0 + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
-                x[1][c] = tile1 >= 0 ? __ldg(r1 + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
-            }
-        };
-        int row0 = tile_of(entry(0, 0)), row1 = tile_of(entry(0, 1));
-        fetch(hi, row0, row1, 0);
-        fetch(lo, row0, row1, D / 8);
-        int next0 = entry(1, 0), next1 = entry(1, 1);
-        for (int tile = 0; tile < p.tiles; ++tile) {
-            const int first = chunk * per_cta + tile * kSelTile + warp * 16;
-            if (first >= nb)
-                break;
-            const bool ok[2] = {row0 >= 0, row1 >= 0};
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-                if (!ok[r] && first + g + 8 * r < nb && t == 0 && h == 0)
-                    atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
-            row0 = tile_of(next0);
-            row1 = tile_of(next1);
-            next0 = entry(tile + 2, 0);
-            next1 = entry(tile + 2, 1);
-            // sc: the scores; ab: the sums of |q+ kmax| and |q- kmin|
-            float sc[4] = {0.f, 0.f, 0.f, 0.f}, ab[4] = {0.f, 0.f, 0.f, 0.f};
-            auto product = [&](const uint4& x, const uint4& y, uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3) {
-                constexpr uint32_t M = 0x7fff7fffu;
-                float c[4];
-                mma_bf16_zero(c, x.x, y.x, x.y, y.y, b0, b1);
-                mma_bf16(c, x.z, y.z, x.w, y.w, b2, b3);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sc[i] += c[i];
-                mma_bf16(ab, x.x & M, y.x & M, x.y & M, y.y & M, b0 & M, b1 & M);
-                mma_bf16(ab, x.z & M, y.z & M, x.w & M, y.w & M, b2 & M, b3 & M);
-            };
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-                product(hi[0][c], hi[1][c], plus(qw[c][0]), plus(qw[c][1]), plus(qw[c][2]), plus(qw[c][3]));
-            fetch(hi, row0, row1, 0);
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-                product(lo[0][c], lo[1][c], minus(qw[c][0]), minus(qw[c][1]), minus(qw[c][2]), minus(qw[c][3]));
-            fetch(lo, row0, row1, D / 8);
-            // rows first + g (sc 0, 1) and first + g + 8 (sc 2, 3), columns 2t and 2t + 1
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float best = -INFINITY, a = 0.f;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (2 * t + i < G) {
-                        const float x = sc[2 * r + i];
-                        best = fmaxf(best, finite(x) ? x : INFINITY);
-                        a = fmaxf(a, ab[2 * r + i]);
-                    }
-                }
-#pragma unroll
-                for (int o = 1; o < 4; o <<= 1) {
-                    best = fmaxf(best, __shfl_xor_sync(kFullMask, best, o));
-                    a = fmaxf(a, __shfl_xor_sync(kFullMask, a, o));
-                }
-                if (!ok[r])
-                    best = -INFINITY;    // a bad block id: chosen last
-                else if (finite(best))
-                    mag = fmaxf(mag, a);
-                const int j = first + g + 8 * r;
-                if (t == 0 && j < nb)
-                    scores[j] = best;
-            }
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1)
-            mag = fmaxf(mag, __shfl_xor_sync(kFullMask, mag, o));
-        if (lane == 0)
-            fscratch[warp] = mag;
-    }
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-        float m = 0.f;
-        for (int i = 0; i < kSelWarps; ++i)
-            m = fmaxf(m, fscratch[i]);
-        p.magnitude[(long long)stream * p.chunks + chunk] = m;
-        __threadfence();
-        const int before = atomicAdd(p.arrived + stream, 1);
-        if (before == active - 1)
-            p.arrived[stream] = 0;       // for the next call
-        bcast[0] = before == active - 1;
-    }
-    __syncthreads();
-    if (!bcast[0])
-        return;
-
-    // ---- selection, by the stream's last CTA
-    __threadfence();
     const bool in_smem = nb <= kSelSmemKeys;
     uint32_t* keys = in_smem ? smem_keys : reinterpret_cast<uint32_t*>(scores);
     const int need = p.keep - p.sink - p.recent;   // among blocks [sink, nb - recent), more than `need` of them
     float mag = 0.f;
     for (int i = tid; i < active; i += kSelThreads)
-        mag = fmaxf(mag, __ldcg(p.magnitude + (long long)stream * p.chunks + i));
+        mag = fmaxf(mag, __ldcg(p.magnitude + (long long)stream * p.parts + i));
     uint32_t kmin = 0xffffffffu, kmax = 0u;
     for (int j = tid; j < nb; j += kSelThreads) {
         uint32_t k = sort_key(__ldcg(scores + j));
@@ -564,19 +621,18 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
 }
 
 struct SelectLayout {
-    size_t arrived, magnitude, scores, near_list, near_score, bytes;
+    size_t magnitude, scores, near_list, near_score, bytes;
 };
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// chunks of the widest grid (one tile per CTA)
+// (a stage has at least 16 blocks, so a stream at most one part for every 16)
 SelectLayout select_layout(long long streams, long long max_blocks)
 {
     SelectLayout l;
-    const size_t chunks = (size_t)((max_blocks + kSelTile - 1) / kSelTile);
-    l.arrived = kWorkspaceHeader;
-    l.magnitude = l.arrived + (size_t)kSelMaxStreams * 4;
-    l.scores = l.magnitude + up256((size_t)streams * chunks * 4);
+    const size_t parts = (size_t)((max_blocks + 15) / 16) + kScoreWarps;
+    l.magnitude = kWorkspaceHeader;
+    l.scores = l.magnitude + up256((size_t)streams * parts * 4);
     l.near_list = l.scores + up256((size_t)streams * max_blocks * 4);
     l.near_score = l.near_list + up256((size_t)streams * max_blocks * 4);
     l.bytes = l.near_score + up256((size_t)streams * max_blocks * 8);
@@ -586,17 +642,43 @@ SelectLayout select_layout(long long streams, long long max_blocks)
 bool select_sizes_ok(int num_seqs, int num_kv_heads, int max_blocks)
 {
     return num_seqs >= 0 && num_seqs <= kMaxSeqs && num_kv_heads > 0 && max_blocks > 0 &&
-           (long long)num_seqs * num_kv_heads <= kSelMaxStreams && (long long)num_seqs * num_kv_heads * max_blocks < (1ll << 31);
+           (long long)num_seqs * num_kv_heads * max_blocks < (1ll << 31);
 }
 
 template <int D, int G>
-int launch_select(const SelectArgs& p, int num_seqs, cudaStream_t stream)
+int launch_select(SelectArgs p, int num_seqs, cudaStream_t stream)
 {
-    auto kern = select_blocks_kernel<D, G>;
-    const int n = p.max_blocks < kSelSmemKeys ? p.max_blocks : kSelSmemKeys;
-    const long long grid = (long long)num_seqs * p.num_kv_heads * p.chunks;
-    kern<<<(unsigned)grid, kSelThreads, (size_t)n * 4, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_LAUNCH;
+    auto score = score_blocks_kernel<D, G>;
+    auto select = select_blocks_kernel<D, G>;
+    p.heads = p.num_kv_heads < kScoreWarps ? p.num_kv_heads : kScoreWarps;
+    p.head_groups = (p.num_kv_heads + p.heads - 1) / p.heads;
+    p.tiles = kScoreWarps / p.heads;
+    const int stage_blocks = 16 * p.tiles;
+    const int stages = (p.max_blocks + stage_blocks - 1) / stage_blocks;
+    // stages a CTA takes: as many as leave six CTAs an SM, up to eight
+    const long long all = (long long)num_seqs * p.head_groups * stages;
+    p.rounds = (int)(all / (148 * 6));
+    p.rounds = p.rounds < 1 ? 1 : (p.rounds > 8 ? 8 : p.rounds);
+    p.chunks = (stages + p.rounds - 1) / p.rounds;
+    p.parts = p.chunks * p.tiles;
+    const size_t smem = (size_t)kScoreStages * stage_blocks * (p.heads * 4 * D + kRowPad) + kScoreStages * 16 +
+                        kScoreStages * 16 * kScoreWarps * 4 + 16;
+    if (!ensure_smem_attribute((const void*)score, smem))
+        return PKV_ERR_LAUNCH;
+    score<<<(unsigned)((long long)num_seqs * p.head_groups * p.chunks), kScoreThreads, smem, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess)
+        return PKV_ERR_LAUNCH;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(num_seqs * p.num_kv_heads));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = (size_t)(p.max_blocks < kSelSmemKeys ? p.max_blocks : kSelSmemKeys) * 4;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, select, p) == cudaSuccess ? PKV_OK : PKV_ERR_LAUNCH;
 }
 
 template <int D>
@@ -661,7 +743,6 @@ PKV_API int select_blocks(int32_t* selected, const void* q, const void* key_boun
     p.block_tables = block_tables;
     p.seq_lens = seq_lens;
     p.err = reinterpret_cast<int32_t*>(ws);
-    p.arrived = reinterpret_cast<int32_t*>(ws + l.arrived);
     p.magnitude = reinterpret_cast<float*>(ws + l.magnitude);
     p.scores = reinterpret_cast<float*>(ws + l.scores);
     p.near_list = reinterpret_cast<int32_t*>(ws + l.near_list);
@@ -674,12 +755,6 @@ PKV_API int select_blocks(int32_t* selected, const void* q, const void* key_boun
     p.keep = num_selected;
     p.sink = num_sink_blocks;
     p.recent = num_recent_blocks;
-    // tiles per CTA: up to 4 where the grid stays above six CTAs an SM without them
-    const long long all_tiles = streams * ((max_blocks_per_seq + kSelTile - 1) / kSelTile);
-    const int kTilesEnv = getenv("PKV_T") ? atoi(getenv("PKV_T")) : 4;
-    p.tiles = (int)(all_tiles / (148 * 6));
-    p.tiles = p.tiles < 1 ? 1 : (p.tiles > kTilesEnv ? kTilesEnv : p.tiles);
-    p.chunks = (max_blocks_per_seq + kSelTile * p.tiles - 1) / (kSelTile * p.tiles);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return head_dim == 128 ? select_by_group<128>(group, p, num_seqs, st) : select_by_group<64>(group, p, num_seqs, st);
 }

@@ -139,17 +139,17 @@ def select(lib, **kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(S=-1), SHAPE), (dict(Hq=6), SHAPE), (dict(Hq=9), SHAPE), (dict(D=256), SHAPE), (dict(BS=5), SHAPE),
     (dict(MB=0), SHAPE), (dict(NB=0), SHAPE), (dict(W=0), SHAPE), (dict(sink=-1), SHAPE), (dict(rec=-1), SHAPE),
-    (dict(sink=3, rec=2), SHAPE), (dict(S=16384, Hkv=32, Hq=32), SHAPE), (dict(o=None), NULL), (dict(b=None), NULL),
-    (dict(ws=None), WS), (dict(wsb=4096), WS), (dict(q=P + 2), SHAPE), (dict(S=0, o=None), 0)])
+    (dict(sink=3, rec=2), SHAPE), (dict(S=16385), SHAPE), (dict(NB=1 << 30), SHAPE), (dict(o=None), NULL), (dict(b=None), NULL),
+    (dict(ws=None), WS), (dict(wsb=512), WS), (dict(q=P + 2), SHAPE), (dict(S=0, o=None), 0)])
 def test_select_refusals(lib, kw, want):
     assert select(lib, **kw) == want
 
 
 def test_select_workspace_size(lib):
     one = lib.pkv_select_workspace_size(1, 1, 1)
-    assert one > 4 << 18                       # the counters' room does not depend on the call
+    assert one >= 256
     assert lib.pkv_select_workspace_size(64, 8, 2048) >= one + 64 * 8 * 2048 * 16
-    for bad in ((-1, 8, 4), (4, 0, 4), (4, 8, 0), (16384, 17, 4), (16384, 16, 1 << 20)):
+    for bad in ((-1, 8, 4), (4, 0, 4), (4, 8, 0), (20000, 1, 4), (16384, 16, 1 << 20)):
         assert lib.pkv_select_workspace_size(*bad) == 0
     with pytest.raises(pkv.PkvError):
         pkv.select_workspace_size(4, 0, 4)
