@@ -24,7 +24,9 @@
 // Two launches. The first streams the bounds: a block's bounds of neighbouring KV heads are one run of
 // memory, so a producer warp brings 16 blocks (or a few times 16) of up to four heads at a time into
 // a ring of shared-memory stages by bulk copies, and a warp per head and 16 blocks turns them into
-// scores. The second, queued behind it as a dependent launch, selects: a CTA per stream.
+// scores. Two CTAs an SM share all stages of the batch evenly, each a range of them. The second,
+// queued behind it as a dependent launch, selects, a CTA per stream: up to 2048 blocks are kept in
+// registers, eight a thread, with as few exchanges as the steps allow (latency is all it costs).
 #include <cstdint>
 
 #include "device.cuh"
@@ -40,7 +42,8 @@ constexpr int kScoreStages = 3;
 constexpr int kRowPad = 64;                   // bytes behind a block's run: neighbouring rows meet other banks
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelSmemKeys = 8192;            // streams of up to this many blocks are selected in shared memory
+constexpr int kSelPerThread = 8;              // keys a thread holds: streams of up to 2048 blocks
+constexpr int kSelSmemKeys = 8192;            // longer ones are selected in shared memory up to this many
 constexpr float kSelError = 7.62939453125e-06f;   // 2^-17
 constexpr uint32_t kChosen = 0xffffffffu;
 
@@ -51,16 +54,15 @@ struct SelectArgs {
     const int32_t* block_tables;
     const int32_t* seq_lens;
     int32_t* err;
-    float* magnitude;             // [streams][parts]: largest A of a warp's share
+    float* magnitude;             // [streams][runs]: the largest A of a run of 16 blocks
     float* scores;                // [streams][max_blocks]
     int32_t* near_list;           // [streams][max_blocks]: blocks near the border
     double* near_score;           // [streams][max_blocks]
-    int num_heads, num_kv_heads, max_blocks, num_blocks, block_size;
+    int num_seqs, num_heads, num_kv_heads, max_blocks, num_blocks, block_size;
     int keep, sink, recent;
-    int heads, head_groups;       // KV heads a scoring CTA takes (the last group may have fewer)
+    int heads, head_groups;       // KV heads a stage holds (the last group may have fewer)
     int tiles;                    // runs of 16 blocks in a stage
-    int rounds, chunks;           // stages a scoring CTA takes, such CTAs for the widest sequence
-    int parts;                    // chunks * tiles
+    int runs;                     // runs of 16 blocks of the widest sequence
 };
 
 // Tokens of sequence s as the table can hold them.
@@ -166,31 +168,68 @@ __device__ __forceinline__ int block_scan(int v, int* scratch, int& total)
     return base + x - v;
 }
 
-// The exact score of a block (a warp): fp64 sums, the largest over the group's query heads.
-template <int D>
-__device__ __forceinline__ double exact_score(const __nv_bfloat16* q, const __nv_bfloat16* bounds, int group, int lane)
+// Stages of one head group of sequence s: none where everything is kept.
+__device__ __forceinline__ int stages_of(const SelectArgs& p, int s)
 {
-    constexpr int E = D / 32;
-    double hi[E], lo[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        hi[e] = (double)__bfloat162float(bounds[lane * E + e]);
-        lo[e] = (double)__bfloat162float(bounds[D + lane * E + e]);
+    const int nb = (held_tokens(p, s) + p.block_size - 1) / p.block_size;
+    return nb <= p.keep ? 0 : (nb + 16 * p.tiles - 1) / (16 * p.tiles);
+}
+
+// A CTA's place in the batch's stages, in (sequence, head group, stage) order.
+struct Walk {
+    int s, hg, r, n;     // stage r of n of head group hg of sequence s
+    __device__ __forceinline__ void next(const SelectArgs& p)
+    {
+        if (++r < n)
+            return;
+        r = 0;
+        if (++hg < p.head_groups)
+            return;
+        hg = 0;
+        for (n = 0; n == 0 && ++s < p.num_seqs;)
+            n = stages_of(p, s);
     }
-    double best = 0.0;
-    for (int g = 0; g < group; ++g) {
-        double s = 0.0;
+};
+
+// Stages of the whole batch; `at` = where stage number `share` of `shares` equal parts begins, and
+// `count` how many it has. A whole warp; sequences are summed in 32 runs, then within the run.
+__device__ __forceinline__ void find_share(const SelectArgs& p, int share, int shares, int lane, Walk& at, int& count)
+{
+    int lo = 0, n = p.num_seqs;
+    long long before = 0, target = -1;
+    count = 0;
+    while (n > 0) {
+        const int per = (n + 31) / 32;
+        int mine = 0;
+        for (int i = lane * per; i < min(n, (lane + 1) * per); ++i)
+            mine += stages_of(p, lo + i) * p.head_groups;
+        long long upto = mine;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const double x = (double)__bfloat162float(q[g * D + lane * E + e]);
-            s = fma(x, x > 0.0 ? hi[e] : lo[e], s);
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(kFullMask, upto, o);
+            if (lane >= o)
+                upto += y;
         }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1)
-            s += __shfl_xor_sync(kFullMask, s, o);
-        best = g == 0 ? s : fmax(best, s);
+        if (target < 0) {                // the first time: the whole batch
+            const long long total = __shfl_sync(kFullMask, upto, 31);
+            target = total * share / shares;
+            count = (int)(total * (share + 1) / shares - target);
+            if (count == 0)
+                return;
+        }
+        const unsigned past = __ballot_sync(kFullMask, before + upto > target);   // some lane: target < total
+        const int l = __ffs(past) - 1;
+        before += __shfl_sync(kFullMask, upto - mine, l);
+        lo += l * per;
+        n = min(per, n - l * per);
+        if (n == 1 && per == 1)
+            break;
     }
-    return best;
+    at.s = lo;
+    at.n = stages_of(p, lo);
+    const int in = (int)(target - before);
+    at.hg = in / at.n;
+    at.r = in - at.hg * at.n;
 }
 
 template <int D, int G>
@@ -209,47 +248,56 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_blocks_kernel(const Se
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int chunk = blockIdx.x % p.chunks, hg = blockIdx.x / p.chunks % p.head_groups;
-    const int s = blockIdx.x / p.chunks / p.head_groups;
-    const int h0 = hg * p.heads, heads = min(p.heads, p.num_kv_heads - h0);
-    const int L = __ldg(p.seq_lens + s);
-    if ((L < 0 || L > p.max_blocks * p.block_size) && chunk == 0 && hg == 0 && tid == 0)
-        atomicOr(p.err, PKV_DEVERR_SEQ_LEN);
-    const int nb = (held_tokens(p, s) + p.block_size - 1) / p.block_size;
-    const int begin = chunk * p.rounds * stage_blocks;
-    if (nb <= p.keep || begin >= nb)     // nothing to choose, or not here
-        return;
-    const int end = min(nb, begin + p.rounds * stage_blocks);
-    const int active = heads * p.tiles;  // warps with work
-
+    for (int i = blockIdx.x * kScoreThreads + tid; i < p.num_seqs; i += gridDim.x * kScoreThreads) {
+        const int L = __ldg(p.seq_lens + i);
+        if (L < 0 || L > p.max_blocks * p.block_size)
+            atomicOr(p.err, PKV_DEVERR_SEQ_LEN);
+    }
     if (tid == 0) {
         for (int i = 0; i < kScoreStages; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], active);
+            mbar_init(&empty[i], kScoreWarps);
         }
         *abort_flag = 0;
         fence_mbar_init();
     }
+    Walk at{};
+    int count;
+    find_share(p, blockIdx.x, gridDim.x, lane, at, count);
     __syncthreads();
-    const int32_t* table = p.block_tables + (long long)s * p.max_blocks;
 
     if (warp == kScoreWarps) {           // the producer: lanes share a stage's blocks
-        auto entry = [&](int j) -> int { return j < end ? __ldg(table + j) : -1; };
-        int next[2] = {entry(begin + lane), entry(begin + 32 + lane)};   // a stage has at most 64 blocks
+        // (a stage has at most 64 blocks)
+        auto entry = [&](const Walk& w, int i) -> int {
+            const int j = w.r * stage_blocks + lane + 32 * i;
+            const int nb = (held_tokens(p, w.s) + p.block_size - 1) / p.block_size;
+            if (lane + 32 * i >= stage_blocks || j >= nb)
+                return -2;               // no block
+            return __ldg(p.block_tables + (long long)w.s * p.max_blocks + j);
+        };
+        int next[2] = {-2, -2};
+        if (count > 0) {
+            next[0] = entry(at, 0);
+            next[1] = entry(at, 1);
+        }
         bool aborted = false;
         int k = 0;
-        for (int base = begin; base < end && !aborted; base += stage_blocks, ++k) {
-            const int st = k % kScoreStages, n = min(stage_blocks, end - base);
+        for (; k < count; ++k) {
+            const int st = k % kScoreStages;
+            const int h0 = at.hg * p.heads, heads = min(p.heads, p.num_kv_heads - h0);
+            const bool first_group = at.hg == 0;
             const int phys[2] = {next[0], next[1]};
-            next[0] = entry(base + stage_blocks + lane);
-            next[1] = entry(base + stage_blocks + 32 + lane);
+            if (k + 1 < count) {         // the next stage's entries come while this one's copies are issued
+                at.next(p);
+                next[0] = entry(at, 0);
+                next[1] = entry(at, 1);
+            }
             bool ok[2];
             int copies = 0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const bool mine = lane + 32 * i < n;
-                ok[i] = mine && phys[i] >= 0 && phys[i] < p.num_blocks;
-                if (mine && !ok[i] && hg == 0)
+                ok[i] = phys[i] >= 0 && phys[i] < p.num_blocks;
+                if (phys[i] != -2 && !ok[i] && first_group)
                     atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
                 copies += __popc(__ballot_sync(kFullMask, ok[i]));
             }
@@ -286,35 +334,36 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_blocks_kernel(const Se
         }
         return;
     }
-    if (warp >= active)
-        return;
-
-    // ---- a consumer: KV head h0 + warp % heads, run warp / heads of each stage
-    const int hw = warp % heads, tile = warp / heads, h = h0 + hw;
-    const long long stream = (long long)s * p.num_kv_heads + h;
-    const __nv_bfloat16* q = p.q + ((long long)s * p.num_heads + (long long)h * G) * D;
-    float* scores = p.scores + stream * p.max_blocks;
+    // ---- a consumer: of each stage KV head warp % heads, run warp / heads
     const int g = lane >> 2, t = lane & 3;
     uint32_t qp[NC][4], qn[NC][4];       // q+ and q- of column g in the order of the bounds' pieces
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (g < G)
-            u = __ldg(reinterpret_cast<const uint4*>(q + (long long)g * D) + 4 * c + t);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
-            const __nv_bfloat162 a = __hmax2_nan(x, zero), b = __hmin2_nan(x, zero);
-            qp[c][i] = *reinterpret_cast<const uint32_t*>(&a);
-            qn[c][i] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-    }
-    float mag = 0.f;
-    int k = 0;
-    for (int base = begin; base < end; base += stage_blocks, ++k) {
+    long long stream = -1;               // the one qp and qn are of
+    for (int k = 0; k < count; ++k, at.next(p)) {
         const int st = k % kScoreStages;
+        const int h0 = at.hg * p.heads, heads = min(p.heads, p.num_kv_heads - h0);
+        const int tile = warp / heads, hw = warp - tile * heads, h = h0 + hw;
+        const int nb = (held_tokens(p, at.s) + p.block_size - 1) / p.block_size;
+        const int first = at.r * stage_blocks + tile * 16;
+        const bool active = tile < p.tiles && first < nb;
+        if (active && stream != (long long)at.s * p.num_kv_heads + h) {
+            stream = (long long)at.s * p.num_kv_heads + h;
+            const __nv_bfloat16* q = p.q + ((long long)at.s * p.num_heads + (long long)h * G) * D;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                if (g < G)
+                    u = __ldg(reinterpret_cast<const uint4*>(q + (long long)g * D) + 4 * c + t);
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+                    const __nv_bfloat162 a = __hmax2_nan(x, zero), b = __hmin2_nan(x, zero);
+                    qp[c][i] = *reinterpret_cast<const uint32_t*>(&a);
+                    qn[c][i] = *reinterpret_cast<const uint32_t*>(&b);
+                }
+            }
+        }
         const bool arrived = !*abort_flag && mbar_wait_bounded(&full[st], (k / kScoreStages) & 1);
         if (!__all_sync(kFullMask, arrived)) {
             if (lane == 0) {
@@ -323,7 +372,11 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_blocks_kernel(const Se
             }
             break;
         }
-        const int first = base + tile * 16;
+        if (!active) {
+            if (lane == 0)
+                mbar_arrive(&empty[st]);
+            continue;
+        }
         const int slot = st * stage_blocks + tile * 16 + g;
         const bool ok[2] = {held[slot] != 0, held[slot + 8] != 0};   // rows g and g + 8
         // sc: the scores; ab and an: the sums of |q+ kmax| and of -|q- kmin|. Rows without a block hold
@@ -352,6 +405,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_blocks_kernel(const Se
         if (lane == 0)
             mbar_arrive(&empty[st]);
         // rows first + g (sc 0, 1) and first + g + 8 (sc 2, 3), columns 2t and 2t + 1
+        float mag = 0.f;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             float best = -INFINITY, a = 0.f;
@@ -373,15 +427,295 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_blocks_kernel(const Se
             else if (finite(best))
                 mag = fmaxf(mag, a);
             const int j = first + g + 8 * r;
-            if (t == 0 && j < end)
-                scores[j] = best;
+            if (t == 0 && j < nb)
+                p.scores[stream * p.max_blocks + j] = best;
+        }
+        mag = __uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(mag)));   // (not negative)
+        if (lane == 0)
+            p.magnitude[stream * p.runs + first / 16] = mag;
+    }
+}
+
+// The exact score of a block: fp64 sums, the largest over the group's query heads (a whole warp).
+template <int D, int G>
+__device__ __forceinline__ double exact_score(const __nv_bfloat16* q, const __nv_bfloat16* bounds, int lane)
+{
+    constexpr int E = D / 32;            // 4 or 2 elements of a row
+    __nv_bfloat16 hi[E], lo[E], x[G][E];
+    auto load = [&](__nv_bfloat16(&to)[E], const __nv_bfloat16* from) {
+        if constexpr (E == 4)
+            *reinterpret_cast<uint2*>(to) = __ldg(reinterpret_cast<const uint2*>(from) + lane);
+        else
+            *reinterpret_cast<uint32_t*>(to) = __ldg(reinterpret_cast<const uint32_t*>(from) + lane);
+    };
+    load(hi, bounds);
+    load(lo, bounds + D);
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+        load(x[g], q + g * D);
+    double best = 0.0;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        double s = 0.0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float f = __bfloat162float(x[g][e]);
+            s = fma((double)f, (double)__bfloat162float(f > 0.f ? hi[e] : lo[e]), s);
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1)
+            s += __shfl_xor_sync(kFullMask, s, o);
+        best = g == 0 ? s : fmax(best, s);
+    }
+    return best;
+}
+
+// The keys from `up` on are certainly above a border `key`, those below `down` certainly not: two
+// errors (the border's own and the block's) and the rounding of this very sum.
+__device__ __forceinline__ void border_zone(uint32_t key, float mag, uint32_t& down, uint32_t& up)
+{
+    const float f = __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+    up = down = key;
+    if (finite(f)) {
+        const float d = 2.f * kSelError * mag + fabsf(f) * 2.4e-7f;
+        up = max(key, sort_key(f + d));
+        down = min(key, sort_key(f - d));
+    }
+}
+
+// A near block's score in 64 bits (a whole warp); one that is not finite in fp32 keeps its place above
+// or below all.
+template <int D, int G>
+__device__ __forceinline__ double near_score_of(const SelectArgs& p, const __nv_bfloat16* q, const int32_t* table, int h,
+                                                int j, uint32_t key, int lane)
+{
+    if (key >= sort_key(INFINITY))
+        return INFINITY;
+    if (key <= sort_key(-INFINITY))
+        return -INFINITY;
+    const long long tile = (long long)__ldg(table + j) * p.num_kv_heads + h;
+    return exact_score<D, G>(q, p.bounds + tile * (2 * D), lane);
+}
+
+struct FastShared {
+    int hist[4][256];
+    int taken[4];                        // keys gathered after each pass; [3]: near blocks
+    uint32_t list[32];
+    uint32_t reduce[3][kSelWarps];
+    int above[kSelWarps];
+    int near_block[kSelThreads];
+    uint32_t near_key[kSelThreads];
+    unsigned long long near_val[kSelThreads];
+    uint32_t chosen[kSelThreads * kSelPerThread / 32];
+    int counts[kSelPerThread * kSelWarps];
+};
+
+// Selection among up to kSelThreads * kSelPerThread blocks by the CTA; thread t holds the keys of blocks
+// t, t + 256, ... Returns false, having written nothing, if more blocks than threads are too close to
+// the border.
+template <int D, int G>
+__device__ __forceinline__ bool select_in_registers(const SelectArgs& p, const __nv_bfloat16* q, const int32_t* table,
+                                                    const float* scores, const float* magnitude, int nb, int h,
+                                                    int32_t* out, FastShared& sh)
+{
+    constexpr int K = kSelPerThread;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int need = p.keep - p.sink - p.recent;
+    uint32_t keys[K];
+    float score[K];
+    float mag = 0.f;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        const int j = i * kSelThreads + tid;
+        score[i] = j < nb ? __ldcg(scores + j) : 0.f;
+    }
+    for (int i = tid; i < (nb + 15) / 16; i += kSelThreads)
+        mag = fmaxf(mag, __ldcg(magnitude + i));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        sh.hist[i][tid] = 0;
+    if (tid < 4)
+        sh.taken[tid] = 0;
+    if (tid < kSelThreads * K / 32)
+        sh.chosen[tid] = 0u;
+    uint32_t kmin = 0xffffffffu, kmax = 0u;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        const int j = i * kSelThreads + tid;
+        keys[i] = j < nb ? sort_key(score[i]) : 0u;      // behind the last block: below every key
+        if (j < p.sink || (j < nb && j >= nb - p.recent)) {
+            keys[i] = kChosen;
+        } else if (j < nb) {
+            kmin = min(kmin, keys[i]);
+            kmax = max(kmax, keys[i]);
         }
     }
+    kmin = __reduce_min_sync(kFullMask, kmin);
+    kmax = __reduce_max_sync(kFullMask, kmax);
+    const uint32_t m0 = __reduce_max_sync(kFullMask, __float_as_uint(mag));   // (not negative)
+    if (lane == 0) {
+        sh.reduce[0][warp] = kmin;
+        sh.reduce[1][warp] = kmax;
+        sh.reduce[2][warp] = m0;
+    }
+    __syncthreads();
+    uint32_t mbits = 0u;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1)
-        mag = fmaxf(mag, __shfl_xor_sync(kFullMask, mag, o));
-    if (lane == 0)
-        p.magnitude[stream * p.parts + chunk * p.tiles + tile] = mag;
+    for (int i = 0; i < kSelWarps; ++i) {
+        kmin = min(kmin, sh.reduce[0][i]);
+        kmax = max(kmax, sh.reduce[1][i]);
+        mbits = max(mbits, sh.reduce[2][i]);
+    }
+    mag = __uint_as_float(mbits);
+
+    uint32_t take = kChosen;             // keys from here on are chosen
+    if (need > 0) {
+        // The border, the need-th largest key: 256 equal bins over the range left, then over the bin
+        // it lies in, until that holds few. Every warp reads the counts for itself.
+        uint32_t lo = kmin, hi = kmax;
+        int rank = need;                 // the rank-th largest of the keys in [lo, hi]
+        int left = nb;
+#pragma unroll 1
+        for (int pass = 0; pass < 4 && lo < hi && left > 32; ++pass) {
+            const uint32_t span = hi - lo;
+            const int shift = span < 256u ? 0 : 24 - __clz(span);
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+                if (keys[i] >= lo && keys[i] <= hi)
+                    atomicAdd(&sh.hist[pass][(keys[i] - lo) >> shift], 1);
+            __syncthreads();
+            // lane l adds up bins 255 - 8 l .. 248 - 8 l, the largest keys first
+            int c[8], sum = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                c[i] = sh.hist[pass][255 - 8 * lane - i];
+                sum += c[i];
+            }
+            int upto = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kFullMask, upto, o);
+                if (lane >= o)
+                    upto += y;
+            }
+            const int l = __ffs(__ballot_sync(kFullMask, upto >= rank)) - 1;
+            int before = upto - sum, bin = 0, in = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (in == 0 && before + c[i] >= rank) {
+                    bin = 255 - 8 * lane - i;
+                    in = c[i];
+                } else if (in == 0) {
+                    before += c[i];
+                }
+            }
+            bin = __shfl_sync(kFullMask, bin, l);
+            left = __shfl_sync(kFullMask, in, l);
+            rank -= __shfl_sync(kFullMask, before, l);
+            const uint32_t base = lo + ((uint32_t)bin << shift);
+            const uint32_t last = base + ((1u << shift) - 1u);
+            hi = last < base || last > hi ? hi : last;
+            lo = base;
+        }
+        if (lo < hi) {                   // at most 32 keys are left: ranked against one another
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+                if (keys[i] >= lo && keys[i] <= hi) {
+                    const int at = atomicAdd(&sh.taken[0], 1);
+                    if (at < 32)
+                        sh.list[at] = keys[i];
+                }
+            __syncthreads();
+            const int n = min(sh.taken[0], 32);
+            const uint32_t mine = lane < n ? sh.list[lane] : 0u;
+            int greater = 0, equal = 0;
+            for (int i = 0; i < n; ++i) {
+                const uint32_t k = __shfl_sync(kFullMask, mine, i);
+                greater += k > mine;
+                equal += k == mine;
+            }
+            const unsigned hit = __ballot_sync(kFullMask, lane < n && greater < rank && rank <= greater + equal);
+            lo = __shfl_sync(kFullMask, mine, __ffs(hit) - 1);
+        }
+        uint32_t down, up;
+        border_zone(lo, mag, down, up);
+        int above = 0;
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            above += keys[i] > up && keys[i] != kChosen;
+            if (keys[i] >= down && keys[i] <= up) {
+                const int at = atomicAdd(&sh.taken[3], 1);
+                if (at < kSelThreads) {
+                    sh.near_block[at] = i * kSelThreads + tid;
+                    sh.near_key[at] = keys[i];
+                }
+            }
+        }
+        above = __reduce_add_sync(kFullMask, above);
+        if (lane == 0)
+            sh.above[warp] = above;
+        __syncthreads();
+        const int near = sh.taken[3];
+        int want = need;                 // of the near ones; 1 <= want <= near
+#pragma unroll
+        for (int i = 0; i < kSelWarps; ++i)
+            want -= sh.above[i];
+        take = down;
+        if (want < near) {
+            if (near > kSelThreads)
+                return false;
+            take = up + 1u;
+            for (int i = warp; i < near; i += kSelWarps) {
+                const double v = near_score_of<D, G>(p, q, table, h, sh.near_block[i], sh.near_key[i], lane);
+                if (lane == 0)
+                    sh.near_val[i] = sort_key(v);
+            }
+            __syncthreads();
+            if (tid < near) {            // each is ranked against the others, ties by index
+                const unsigned long long mine = sh.near_val[tid];
+                const int block = sh.near_block[tid];
+                int better = 0;
+                for (int i = 0; i < near; ++i) {
+                    const unsigned long long k = sh.near_val[i];
+                    better += k > mine || (k == mine && sh.near_block[i] < block);
+                }
+                if (better < want)
+                    atomicOr(&sh.chosen[block / 32], 1u << (block % 32));
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+                if (sh.chosen[i * (kSelThreads / 32) + warp] >> lane & 1u)
+                    keys[i] = kChosen;
+        }
+    }
+    // ascending order: by i, then by thread
+    unsigned m[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        m[i] = __ballot_sync(kFullMask, keys[i] >= take);
+        if (lane == 0)
+            sh.counts[i * kSelWarps + warp] = __popc(m[i]);
+    }
+    __syncthreads();
+    const int c0 = sh.counts[2 * lane], c1 = sh.counts[2 * lane + 1];
+    int upto = c0 + c1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFullMask, upto, o);
+        if (lane >= o)
+            upto += y;
+    }
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        const int e = i * kSelWarps + warp;      // entries before this warp's, two a lane
+        const int upto_pair = __shfl_sync(kFullMask, upto, e / 2);
+        const int pair0 = __shfl_sync(kFullMask, c0, e / 2), pair1 = __shfl_sync(kFullMask, c1, e / 2);
+        const int at = upto_pair - pair1 - (e & 1 ? 0 : pair0) + __popc(m[i] & ((1u << lane) - 1u));
+        if ((m[i] >> lane & 1u) && at < p.keep)
+            out[at] = i * kSelThreads + tid;
+    }
+    return true;
 }
 
 template <int D, int G>
@@ -408,15 +742,16 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
     const __nv_bfloat16* q = p.q + ((long long)s * p.num_heads + (long long)h * G) * D;
     const int32_t* table = p.block_tables + (long long)s * p.max_blocks;
     float* scores = p.scores + (long long)stream * p.max_blocks;
-    const int stage_blocks = 16 * p.tiles;
-    const int active = (nb + p.rounds * stage_blocks - 1) / (p.rounds * stage_blocks) * p.tiles;
-
+    const float* magnitude = p.magnitude + (long long)stream * p.runs;
+    __shared__ FastShared fast;
+    if (nb <= kSelThreads * kSelPerThread && select_in_registers<D, G>(p, q, table, scores, magnitude, nb, h, out, fast))
+        return;
     const bool in_smem = nb <= kSelSmemKeys;
     uint32_t* keys = in_smem ? smem_keys : reinterpret_cast<uint32_t*>(scores);
     const int need = p.keep - p.sink - p.recent;   // among blocks [sink, nb - recent), more than `need` of them
     float mag = 0.f;
-    for (int i = tid; i < active; i += kSelThreads)
-        mag = fmaxf(mag, __ldcg(p.magnitude + (long long)stream * p.parts + i));
+    for (int i = tid; i < (nb + 15) / 16; i += kSelThreads)
+        mag = fmaxf(mag, __ldcg(magnitude + i));
     uint32_t kmin = 0xffffffffu, kmax = 0u;
     for (int j = tid; j < nb; j += kSelThreads) {
         uint32_t k = sort_key(__ldcg(scores + j));
@@ -512,15 +847,8 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
             lo = (uint32_t)bcast[1];
         }
         // blocks whose order against that one the fp32 scores do not settle
-        const uint32_t border = lo;
-        const float f = __uint_as_float(border & 0x80000000u ? border & 0x7fffffffu : ~border);
-        uint32_t up = border, down = border;
-        if (finite(f)) {
-            // two errors (the border's own and the block's) and the rounding of this very sum
-            const float d = 2.f * kSelError * mag + fabsf(f) * 2.4e-7f;
-            up = max(border, sort_key(f + d));
-            down = min(border, sort_key(f - d));
-        }
+        uint32_t down, up;
+        border_zone(lo, mag, down, up);
         int above = 0, near = 0;
         for (int j = tid; j < nb; j += kSelThreads) {
             const uint32_t k = keys[j];
@@ -545,19 +873,8 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
                 if (keys[j] >= down && keys[j] <= up)
                     list[at++] = j;
             __syncthreads();
-            // blocks without a finite score (bad ids among them) keep their place above or below all
             for (int i = warp; i < near; i += kSelWarps) {
-                const int j = list[i];
-                const uint32_t k = keys[j];
-                double v;
-                if (k >= sort_key(INFINITY)) {
-                    v = INFINITY;
-                } else if (k <= sort_key(-INFINITY)) {
-                    v = -INFINITY;
-                } else {
-                    const long long tile = (long long)__ldg(table + j) * p.num_kv_heads + h;
-                    v = exact_score<D>(q, p.bounds + tile * (2 * D), G, lane);
-                }
+                const double v = near_score_of<D, G>(p, q, table, h, list[i], keys[list[i]], lane);
                 if (lane == 0)
                     (near <= kSelThreads ? near_vals : val)[i] = v;
             }
@@ -626,11 +943,10 @@ struct SelectLayout {
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// (a stage has at least 16 blocks, so a stream at most one part for every 16)
 SelectLayout select_layout(long long streams, long long max_blocks)
 {
     SelectLayout l;
-    const size_t parts = (size_t)((max_blocks + 15) / 16) + kScoreWarps;
+    const size_t parts = (size_t)((max_blocks + 15) / 16);   // runs of 16 blocks
     l.magnitude = kWorkspaceHeader;
     l.scores = l.magnitude + up256((size_t)streams * parts * 4);
     l.near_list = l.scores + up256((size_t)streams * max_blocks * 4);
@@ -655,17 +971,14 @@ int launch_select(SelectArgs p, int num_seqs, cudaStream_t stream)
     p.tiles = kScoreWarps / p.heads;
     const int stage_blocks = 16 * p.tiles;
     const int stages = (p.max_blocks + stage_blocks - 1) / stage_blocks;
-    // stages a CTA takes: as many as leave six CTAs an SM, up to eight
+    p.runs = (p.max_blocks + 15) / 16;
     const long long all = (long long)num_seqs * p.head_groups * stages;
-    p.rounds = (int)(all / (148 * 6));
-    p.rounds = p.rounds < 1 ? 1 : (p.rounds > 8 ? 8 : p.rounds);
-    p.chunks = (stages + p.rounds - 1) / p.rounds;
-    p.parts = p.chunks * p.tiles;
+    const unsigned grid = (unsigned)(all < 2 * 148 ? all : 2 * 148);
     const size_t smem = (size_t)kScoreStages * stage_blocks * (p.heads * 4 * D + kRowPad) + kScoreStages * 16 +
                         kScoreStages * 16 * kScoreWarps * 4 + 16;
     if (!ensure_smem_attribute((const void*)score, smem))
         return PKV_ERR_LAUNCH;
-    score<<<(unsigned)((long long)num_seqs * p.head_groups * p.chunks), kScoreThreads, smem, stream>>>(p);
+    score<<<grid, kScoreThreads, smem, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess)
         return PKV_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
@@ -747,6 +1060,7 @@ PKV_API int select_blocks(int32_t* selected, const void* q, const void* key_boun
     p.scores = reinterpret_cast<float*>(ws + l.scores);
     p.near_list = reinterpret_cast<int32_t*>(ws + l.near_list);
     p.near_score = reinterpret_cast<double*>(ws + l.near_score);
+    p.num_seqs = num_seqs;
     p.num_heads = num_heads;
     p.num_kv_heads = num_kv_heads;
     p.max_blocks = max_blocks_per_seq;
