@@ -493,6 +493,29 @@ def validate_tables(block_tables, seq_lens, block_size: int, num_blocks: int, sl
     return int(bits.value), int(first.value)
 
 
+# The operators below are called once per layer and step: their checks read each property once.
+
+def _current_raw_stream(dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _raw_stream(stream, dev: int) -> int:
+    if stream is None:
+        return _current_raw_stream(dev)
+    return int(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
+
+
+def _ptr(name, t, dev):
+    """Device pointer of a contiguous CUDA tensor on device `dev`, as _cuda checks it."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    return _cuda(name, t, dev).value
+
+
+def _opt_ptr(name, t, dev):
+    return None if t is None else _ptr(name, t, dev)
+
+
 def _rows(name, t, dev, heads=None, dim=None, dtype=None):
     """(device pointer, tokens, heads, head_dim, token stride) of rows [tokens, heads, head_dim] whose
     heads are contiguous; tokens may lie further apart (a view of a projection's output)."""
@@ -505,22 +528,24 @@ def _rows(name, t, dev, heads=None, dim=None, dtype=None):
         raise ValueError(f"{name} has another number of heads or another head_dim")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if t.device.index != dev:
+    if t.get_device() != dev and t.device.index != dev:
         raise ValueError(f"{name} is on {t.device}, the current CUDA device is cuda:{dev}")
-    if T > 0 and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D)):
+    s0, s1, s2 = t.stride()
+    if T > 0 and (s2 != 1 or (H > 1 and s1 != D)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    if T > 1 and t.stride(0) < H * D:
+    if T > 1 and s0 < H * D:
         raise ValueError(f"{name}: tokens must not share elements")
-    return ctypes.c_void_p(t.data_ptr()), T, H, D, (t.stride(0) if T > 1 else H * D)
+    return t.data_ptr(), T, H, D, (s0 if T > 1 else H * D)
 
 
 def _norm_rope_args(q_out, q, k, q_weight, k_weight, cos_sin, positions, dev):
     """Checked pieces that qk_norm_rope and qk_norm_rope_and_cache share."""
+    dt = q.dtype
     qp, T, Hq, D, qs = _rows("q", q, dev)
-    kp, Tk, Hkv, _, ks = _rows("k", k, dev, dim=D, dtype=q.dtype)
-    if Tk != T or tuple(q_out.shape) != (T, Hq, D):
+    kp, Tk, Hkv, _, ks = _rows("k", k, dev, dim=D, dtype=dt)
+    if Tk != T or q_out.shape != (T, Hq, D):
         raise ValueError("shape mismatch between q, k and q_out")
-    if q_out.dtype != q.dtype or q_weight.dtype != q.dtype or k_weight.dtype != q.dtype:
+    if q_out.dtype != dt or q_weight.dtype != dt or k_weight.dtype != dt:
         raise TypeError("q_out and the weights must have q's dtype")
     if q_weight.shape != (D,) or k_weight.shape != (D,):
         raise ValueError("the weights must be [head_dim]")
@@ -528,7 +553,9 @@ def _norm_rope_args(q_out, q, k, q_weight, k_weight, cos_sin, positions, dev):
         raise TypeError("cos_sin must be float32 [num_positions, rotary_dim]")
     if positions.dtype != torch.int64 or positions.shape != (T,):
         raise TypeError("positions must be int64 [num_tokens]")
-    return qp, kp, T, Hq, Hkv, D, qs, ks
+    return (qp, kp, T, Hq, Hkv, D, qs, ks, _ptr("q_out", q_out, dev), _ptr("q_weight", q_weight, dev),
+            _ptr("k_weight", k_weight, dev), _ptr("cos_sin", cos_sin, dev), _ptr("positions", positions, dev),
+            *cos_sin.shape, _dtype_code(q))
 
 
 def qk_norm_rope(q_out, k_out, q, k, q_weight, k_weight, eps, cos_sin, positions, interleaved=False,
@@ -540,16 +567,13 @@ def qk_norm_rope(q_out, k_out, q, k, q_weight, k_weight, eps, cos_sin, positions
     weights [head_dim]; cos_sin float32 [num_positions, rotary_dim] (cosines, then sines);
     positions int64 [num_tokens]."""
     dev = _launch_device("q", q)
-    qp, kp, T, Hq, Hkv, D, qs, ks = _norm_rope_args(q_out, q, k, q_weight, k_weight, cos_sin, positions, dev)
-    if tuple(k_out.shape) != (T, Hkv, D) or k_out.dtype != q.dtype:
+    qp, kp, T, Hq, Hkv, D, qs, ks, qo, qw, kw, cs, pos, NP, R, dt = _norm_rope_args(
+        q_out, q, k, q_weight, k_weight, cos_sin, positions, dev)
+    if k_out.shape != (T, Hkv, D) or k_out.dtype != q.dtype:
         raise ValueError("k_out must match k")
-    err = ctypes.c_void_p(None) if device_error is None else _cuda("device_error", device_error, dev)
-    st = load_library().qk_norm_rope(
-        _cuda("q_out", q_out, dev), _cuda("k_out", k_out, dev), qp, kp, _cuda("q_weight", q_weight, dev),
-        _cuda("k_weight", k_weight, dev), float(eps), _cuda("cos_sin", cos_sin, dev),
-        _cuda("positions", positions, dev), T, Hq, Hkv, D, cos_sin.shape[1], cos_sin.shape[0], int(bool(interleaved)),
-        qs, ks, _dtype_code(q), err, _stream_handle(stream))
-    _check("qk_norm_rope", st)
+    _check("qk_norm_rope", load_library().qk_norm_rope(
+        qo, _ptr("k_out", k_out, dev), qp, kp, qw, kw, float(eps), cs, pos, T, Hq, Hkv, D, R, NP, bool(interleaved), qs, ks, dt,
+        _opt_ptr("device_error", device_error, dev), _raw_stream(stream, dev)))
 
 
 def qk_norm_rope_and_cache(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, positions, k_cache, v_cache,
@@ -558,45 +582,43 @@ def qk_norm_rope_and_cache(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, pos
     """qk_norm_rope with the append of reshape_and_cache in the same pass: the new keys and the rows
     of v go to slot slot_mapping[t] of the caches (a negative slot appends nothing)."""
     dev = _launch_device("q", q)
-    qp, kp, T, Hq, Hkv, D, qs, ks = _norm_rope_args(q_out, q, k, q_weight, k_weight, cos_sin, positions, dev)
+    qp, kp, T, Hq, Hkv, D, qs, ks, qo, qw, kw, cs, pos, NP, R, dt = _norm_rope_args(
+        q_out, q, k, q_weight, k_weight, cos_sin, positions, dev)
     vp, Tv, _, _, vs = _rows("v", v, dev, heads=Hkv, dim=D, dtype=q.dtype)
-    NB, Hkv2, BS, D2 = k_cache.shape
-    if Tv != T or (Hkv2, D2) != (Hkv, D) or tuple(v_cache.shape) != tuple(k_cache.shape):
+    shape = k_cache.shape
+    NB, Hkv2, BS, D2 = shape
+    if Tv != T or Hkv2 != Hkv or D2 != D or v_cache.shape != shape:
         raise ValueError("shape mismatch between rows and caches")
     if v_cache.dtype != k_cache.dtype:
         raise TypeError("v_cache must have k_cache's dtype")
     if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
         raise TypeError("slot_mapping must be int64 [num_tokens]")
-    err = ctypes.c_void_p(None) if device_error is None else _cuda("device_error", device_error, dev)
-    st = load_library().qk_norm_rope_and_cache(
-        _cuda("q_out", q_out, dev), qp, kp, vp, _cuda("q_weight", q_weight, dev), _cuda("k_weight", k_weight, dev),
-        float(eps), _cuda("cos_sin", cos_sin, dev), _cuda("positions", positions, dev), _cuda("k_cache", k_cache, dev),
-        _cuda("v_cache", v_cache, dev), _cuda("slot_mapping", slot_mapping, dev), T, Hq, Hkv, D, cos_sin.shape[1],
-        cos_sin.shape[0], BS, NB, int(bool(interleaved)), qs, ks, vs, _dtype_code(q), _dtype_code(k_cache),
-        float(k_scale), float(v_scale), err, _stream_handle(stream))
-    _check("qk_norm_rope_and_cache", st)
+    _check("qk_norm_rope_and_cache", load_library().qk_norm_rope_and_cache(
+        qo, qp, kp, vp, qw, kw, float(eps), cs, pos, _ptr("k_cache", k_cache, dev), _ptr("v_cache", v_cache, dev),
+        _ptr("slot_mapping", slot_mapping, dev), T, Hq, Hkv, D, R, NP, BS, NB, bool(interleaved), qs, ks, vs, dt,
+        _dtype_code(k_cache), float(k_scale), float(v_scale), _opt_ptr("device_error", device_error, dev), _raw_stream(stream, dev)))
 
 
 def _tables(block_tables, seq_lens, dev):
     """Checked (block_tables pointer, seq_lens pointer, num_seqs, max_blocks)."""
     if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise TypeError("block_tables and seq_lens must be int32")
-    if block_tables.dim() != 2 or seq_lens.shape != (block_tables.shape[0],):
+    shape = block_tables.shape
+    if len(shape) != 2 or seq_lens.shape != shape[:1]:
         raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
-    return (_cuda("block_tables", block_tables, dev), _cuda("seq_lens", seq_lens, dev), block_tables.shape[0],
-            block_tables.shape[1])
+    return _ptr("block_tables", block_tables, dev), _ptr("seq_lens", seq_lens, dev), shape[0], shape[1]
 
 
-def _block_scales(name, t, cache, dev):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or tuple(t.shape) != tuple(cache.shape[:2]):
+def _block_scales(name, t, cache_shape, dev):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.shape != cache_shape[:2]:
         raise TypeError(f"{name} must be a float32 tensor [num_blocks, num_kv_heads]")
-    return _cuda(name, t, dev)
+    return _ptr(name, t, dev)
 
 
 def _row_offsets(t, S, dev):
     if t.dtype != torch.int32 or t.shape != (S + 1,):
         raise TypeError("row_offsets must be int32 [num_seqs + 1]")
-    return _cuda("row_offsets", t, dev)
+    return _ptr("row_offsets", t, dev)
 
 
 def reshape_and_cache_block_scales(k, v, k_cache, v_cache, k_block_scales, v_block_scales, block_tables, seq_lens,
@@ -610,32 +632,35 @@ def reshape_and_cache_block_scales(k, v, k_cache, v_cache, k_block_scales, v_blo
     dev = _launch_device("k", k)
     kp, T, Hkv, D, ks = _rows("k", k, dev)
     vp, Tv, _, _, vs = _rows("v", v, dev, heads=Hkv, dim=D, dtype=k.dtype)
-    NB, Hkv2, BS, D2 = k_cache.shape
-    if Tv != T or (Hkv2, D2) != (Hkv, D) or tuple(v_cache.shape) != tuple(k_cache.shape):
+    shape = k_cache.shape
+    NB, Hkv2, BS, D2 = shape
+    if Tv != T or Hkv2 != Hkv or D2 != D or v_cache.shape != shape:
         raise ValueError("shape mismatch between rows and caches")
     if v_cache.dtype != k_cache.dtype:
         raise TypeError("v_cache must have k_cache's dtype")
     bt, sl, S, MB = _tables(block_tables, seq_lens, dev)
-    err = ctypes.c_void_p(None) if device_error is None else _cuda("device_error", device_error, dev)
-    st = load_library().reshape_and_cache_block_scales(
-        kp, vp, _cuda("k_cache", k_cache, dev), _cuda("v_cache", v_cache, dev),
-        _block_scales("k_block_scales", k_block_scales, k_cache, dev),
-        _block_scales("v_block_scales", v_block_scales, k_cache, dev), bt, sl, _row_offsets(row_offsets, S, dev), T, S,
-        Hkv, D, BS, MB, NB, ks, vs, _dtype_code(k), _dtype_code(k_cache), err, _stream_handle(stream))
-    _check("reshape_and_cache_block_scales", st)
+    _check("reshape_and_cache_block_scales", load_library().reshape_and_cache_block_scales(
+        kp, vp, _ptr("k_cache", k_cache, dev), _ptr("v_cache", v_cache, dev),
+        _block_scales("k_block_scales", k_block_scales, shape, dev),
+        _block_scales("v_block_scales", v_block_scales, shape, dev), bt, sl, _row_offsets(row_offsets, S, dev), T, S,
+        Hkv, D, BS, MB, NB, ks, vs, _dtype_code(k), _dtype_code(k_cache), _opt_ptr("device_error", device_error, dev),
+        _raw_stream(stream, dev)))
 
 
 def _decode_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, dev):
-    S, Hq, D = q.shape
-    NB, Hkv, BS, D2 = k_cache.shape
-    if D2 != D or tuple(v_cache.shape) != tuple(k_cache.shape) or tuple(out.shape) != tuple(q.shape):
+    """Checked sizes and pointers of a decode: (num_seqs, num_heads, head_dim, cache shape, out, q, k_cache,
+    v_cache, block_tables, seq_lens, max_blocks)."""
+    shape, cache = q.shape, k_cache.shape
+    S, Hq, D = shape
+    if cache[3] != D or v_cache.shape != cache or out.shape != shape:
         raise ValueError("shape mismatch between q/out and the caches")
     if out.dtype != q.dtype or v_cache.dtype != k_cache.dtype:
         raise TypeError("out must match q's dtype and v_cache k_cache's")
     bt, sl, S2, MB = _tables(block_tables, seq_lens, dev)
     if S2 != S:
         raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
-    return S, Hq, D, NB, Hkv, BS, bt, sl, MB
+    return (S, Hq, D, cache, _ptr("out", out, dev), _ptr("q", q, dev), _ptr("k_cache", k_cache, dev),
+            _ptr("v_cache", v_cache, dev), bt, sl, MB)
 
 
 def paged_attention_decode_block_scales(out, q, k_cache, v_cache, block_tables, seq_lens, scale, k_block_scales,
@@ -643,16 +668,16 @@ def paged_attention_decode_block_scales(out, q, k_cache, v_cache, block_tables, 
     """paged_attention_decode over an 8-bit cache with one scale for each (block, KV head):
     k_block_scales, v_block_scales float32 [num_blocks, num_kv_heads], positive."""
     dev = _launch_device("q", q)
-    S, Hq, D, NB, Hkv, BS, bt, sl, MB = _decode_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, dev)
+    S, Hq, D, cache, op, qp, kp, vp, bt, sl, MB = _decode_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, dev)
+    NB, Hkv, BS, _ = cache
+    ks = _block_scales("k_block_scales", k_block_scales, cache, dev)
+    vs = _block_scales("v_block_scales", v_block_scales, cache, dev)
+    st = _raw_stream(stream, dev)
     if workspace is None:
-        workspace = _op_workspace("decode", workspace_size(S, Hq, Hkv, D, num_partitions), 256, dev, stream)
-    st = load_library().paged_attention_decode_block_scales(
-        _cuda("out", out, dev), _cuda("q", q, dev), _cuda("k_cache", k_cache, dev), _cuda("v_cache", v_cache, dev),
-        bt, sl, S, Hq, Hkv, D, BS, float(scale), MB, NB, _dtype_code(q), _dtype_code(k_cache),
-        _block_scales("k_block_scales", k_block_scales, k_cache, dev),
-        _block_scales("v_block_scales", v_block_scales, k_cache, dev), int(num_partitions),
-        _cuda("workspace", workspace, dev), workspace.numel(), _stream_handle(stream))
-    _check("paged_attention_decode_block_scales", st)
+        workspace = _op_workspace("decode", _sized(workspace_size, dev, S, Hq, Hkv, D, num_partitions), dev, st)
+    _check("paged_attention_decode_block_scales", load_library().paged_attention_decode_block_scales(
+        op, qp, kp, vp, bt, sl, S, Hq, Hkv, D, BS, float(scale), MB, NB, _dtype_code(q), _dtype_code(k_cache), ks, vs,
+        int(num_partitions), _ptr("workspace", workspace, dev), workspace.numel(), st))
 
 
 def update_key_bounds(key_bounds, k_cache, block_tables, seq_lens, row_offsets, num_tokens, k_scale=1.0,
@@ -661,18 +686,16 @@ def update_key_bounds(key_bounds, k_cache, block_tables, seq_lens, row_offsets, 
     block's keys) for the blocks that hold the num_tokens newest tokens of a batch, after their
     append; row_offsets as in reshape_and_cache_block_scales (int32 [num_seqs + 1])."""
     dev = _launch_device("k_cache", k_cache)
-    NB, Hkv, BS, D = k_cache.shape
-    if key_bounds.dtype != torch.bfloat16 or tuple(key_bounds.shape) != (NB, Hkv, 2, D):
+    shape = k_cache.shape
+    NB, Hkv, BS, D = shape
+    if key_bounds.dtype != torch.bfloat16 or key_bounds.shape != (NB, Hkv, 2, D):
         raise TypeError("key_bounds must be bfloat16 [num_blocks, num_kv_heads, 2, head_dim]")
     bt, sl, S, MB = _tables(block_tables, seq_lens, dev)
-    scales = ctypes.c_void_p(None) if k_block_scales is None else \
-        _block_scales("k_block_scales", k_block_scales, k_cache, dev)
-    err = ctypes.c_void_p(None) if device_error is None else _cuda("device_error", device_error, dev)
-    st = load_library().update_key_bounds(
-        _cuda("key_bounds", key_bounds, dev), _cuda("k_cache", k_cache, dev), bt, sl, _row_offsets(row_offsets, S, dev),
-        int(num_tokens), S, Hkv, D, BS, MB, NB, _dtype_code(k_cache), float(k_scale), scales, err,
-        _stream_handle(stream))
-    _check("update_key_bounds", st)
+    scales = None if k_block_scales is None else _block_scales("k_block_scales", k_block_scales, shape, dev)
+    _check("update_key_bounds", load_library().update_key_bounds(
+        _ptr("key_bounds", key_bounds, dev), _ptr("k_cache", k_cache, dev), bt, sl, _row_offsets(row_offsets, S, dev),
+        int(num_tokens), S, Hkv, D, BS, MB, NB, _dtype_code(k_cache), float(k_scale), scales,
+        _opt_ptr("device_error", device_error, dev), _raw_stream(stream, dev)))
 
 
 def select_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq) -> int:
@@ -702,18 +725,24 @@ def select_blocks(selected, q, key_bounds, block_tables, seq_lens, block_size, n
         raise TypeError("q and key_bounds must be bfloat16")
     if two != 2 or D2 != D:
         raise ValueError("key_bounds must be [num_blocks, num_kv_heads, 2, head_dim]")
-    if selected.dtype != torch.int32 or selected.dim() != 3 or tuple(selected.shape[:2]) != (S, Hkv):
-        raise TypeError("selected must be int32 [num_seqs, num_kv_heads, num_selected]")
+    W = _selected_width(selected, S, Hkv)
     bt, sl, S2, MB = _tables(block_tables, seq_lens, dev)
     if S2 != S:
         raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
+    st = _raw_stream(stream, dev)
     if workspace is None:
-        workspace = _op_workspace("select", select_workspace_size(S, Hkv, max(1, MB)), 256, dev, stream)
-    st = load_library().select_blocks(
-        _cuda("selected", selected, dev), _cuda("q", q, dev), _cuda("key_bounds", key_bounds, dev), bt, sl, S, Hq, Hkv,
-        D, int(block_size), MB, NB, selected.shape[2], int(num_sink_blocks), int(num_recent_blocks),
-        _cuda("workspace", workspace, dev), workspace.numel(), _stream_handle(stream))
-    _check("select_blocks", st)
+        workspace = _op_workspace("select", _sized(select_workspace_size, dev, S, Hkv, max(1, MB)), dev, st)
+    _check("select_blocks", load_library().select_blocks(
+        _ptr("selected", selected, dev), _ptr("q", q, dev), _ptr("key_bounds", key_bounds, dev), bt, sl, S, Hq, Hkv, D,
+        int(block_size), MB, NB, W, int(num_sink_blocks), int(num_recent_blocks), _ptr("workspace", workspace, dev),
+        workspace.numel(), st))
+
+
+def _selected_width(selected, S, Hkv) -> int:
+    shape = selected.shape
+    if selected.dtype != torch.int32 or len(shape) != 3 or shape[0] != S or shape[1] != Hkv:
+        raise TypeError("selected must be int32 [num_seqs, num_kv_heads, num_selected]")
+    return shape[2]
 
 
 def paged_attention_decode_sparse(out, q, k_cache, v_cache, block_tables, seq_lens, selected, scale, k_scale=1.0,
@@ -723,50 +752,58 @@ def paged_attention_decode_sparse(out, q, k_cache, v_cache, block_tables, seq_le
     num_kv_heads, num_selected] (select_blocks' output), negative entries empty. 8-bit caches take
     per-tensor scales or both block scales."""
     dev = _launch_device("q", q)
-    S, Hq, D, NB, Hkv, BS, bt, sl, MB = _decode_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, dev)
-    if selected.dtype != torch.int32 or selected.dim() != 3 or tuple(selected.shape[:2]) != (S, Hkv):
-        raise TypeError("selected must be int32 [num_seqs, num_kv_heads, num_selected]")
+    S, Hq, D, cache, op, qp, kp, vp, bt, sl, MB = _decode_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, dev)
+    NB, Hkv, BS, _ = cache
+    W = _selected_width(selected, S, Hkv)
     if (k_block_scales is None) != (v_block_scales is None):
         raise ValueError("give both block scales or none")
-    ks = vs = ctypes.c_void_p(None)
+    ks = vs = None
     if k_block_scales is not None:
-        ks = _block_scales("k_block_scales", k_block_scales, k_cache, dev)
-        vs = _block_scales("v_block_scales", v_block_scales, k_cache, dev)
+        ks = _block_scales("k_block_scales", k_block_scales, cache, dev)
+        vs = _block_scales("v_block_scales", v_block_scales, cache, dev)
+    st = _raw_stream(stream, dev)
     if workspace is None:
-        workspace = _op_workspace("decode", workspace_size(S, Hq, Hkv, D, num_partitions), 256, dev, stream)
-    st = load_library().paged_attention_decode_sparse(
-        _cuda("out", out, dev), _cuda("q", q, dev), _cuda("k_cache", k_cache, dev), _cuda("v_cache", v_cache, dev),
-        bt, sl, _cuda("selected", selected, dev), S, Hq, Hkv, D, BS, float(scale), MB, NB, selected.shape[2],
-        _dtype_code(q), _dtype_code(k_cache), float(k_scale), float(v_scale), ks, vs, int(num_partitions),
-        _cuda("workspace", workspace, dev), workspace.numel(), _stream_handle(stream))
-    _check("paged_attention_decode_sparse", st)
+        workspace = _op_workspace("decode", _sized(workspace_size, dev, S, Hq, Hkv, D, num_partitions), dev, st)
+    _check("paged_attention_decode_sparse", load_library().paged_attention_decode_sparse(
+        op, qp, kp, vp, bt, sl, _ptr("selected", selected, dev), S, Hq, Hkv, D, BS, float(scale), MB, NB, W,
+        _dtype_code(q), _dtype_code(k_cache), float(k_scale), float(v_scale), ks, vs, int(num_partitions), _ptr("workspace", workspace, dev),
+        workspace.numel(), st))
+
+
+_sizes: dict = {}
+
+
+def _sized(size, dev, *args) -> int:
+    """size(*args), remembered: a workspace's size depends on these numbers and the device alone."""
+    n = _sizes.get((size, dev, args))
+    if n is None:
+        n = size(*args)
+        if len(_sizes) < 4096:
+            _sizes[(size, dev, args)] = n
+    return n
 
 
 _op_ws: dict = {}
+_OP_HEADER = 256     # what an operator's workspace needs cleared before its first call
 
 
-def _op_workspace(kind, n, zeroed, dev, stream):
-    """A workspace of at least n bytes, its first `zeroed` ones cleared, kept per (kind, device,
-    stream), so that calls on different streams never share one. It is allocated and cleared on the
-    stream that uses it. While that stream is being captured every call gets its own, from the
-    graph's memory and cleared inside the graph: two graphs, or a graph and later eager calls, then
-    never meet in one."""
-    handle = _stream_handle(stream)
-    current = torch.cuda.current_stream()
+def _op_workspace(kind, n, dev, stream):
+    """A workspace of at least n bytes with a clear header, kept per (kind, device, stream), so that
+    calls on different streams never share one. It is allocated and cleared on the stream that uses
+    it. While that stream is being captured every call gets its own, from the graph's memory and
+    cleared inside the graph: two graphs, or a graph and later eager calls, never meet in one."""
     capturing = torch.cuda.is_current_stream_capturing()
-    if capturing and handle.value != ctypes.c_void_p(current.cuda_stream).value:
+    if capturing and stream != _current_raw_stream(dev):
         raise ValueError("pass a workspace to capture on another stream than the current one")
-    key = (kind, dev, handle.value)
-    ws = None if capturing else _op_ws.get(key)
+    ws = None if capturing else _op_ws.get((kind, dev, stream))
     if ws is None or ws.numel() < n:
-        on = current if handle.value == ctypes.c_void_p(current.cuda_stream).value else \
-            torch.cuda.ExternalStream(handle.value or 0, device=dev)
-        with torch.cuda.stream(on):
+        here = stream == _current_raw_stream(dev)
+        with torch.cuda.stream(torch.cuda.current_stream() if here else torch.cuda.ExternalStream(stream, device=dev)):
             ws = torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", dev))
-        _check("pkv_workspace_init",
-               load_library().pkv_workspace_init(_cuda("workspace", ws), min(n, zeroed), handle))
+        _check("pkv_workspace_init", load_library().pkv_workspace_init(_ptr("workspace", ws, dev), min(n, _OP_HEADER),
+                                                                       stream))
         if not capturing:
-            _op_ws[key] = ws
+            _op_ws[(kind, dev, stream)] = ws
     return ws
 
 

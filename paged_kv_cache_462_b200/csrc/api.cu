@@ -450,6 +450,13 @@ int heads_impl(void* out, const void* q, const void* k_cache, const void* v_cach
         if (occ < 1)
             return PKV_ERR_SHAPE;
         runs = sms * (occ > kMaxRunsPerSM ? kMaxRunsPerSM : occ);
+        // Few units: four to a run, not one. A run's copies are in flight together, so more units cost it
+        // little, while every run leaves a piece of each stream to merge (one sequence, 64 selected
+        // blocks: 13 us with 32 runs, 20 us with 296).
+        const long long width = selected && num_selected < max_blocks_per_seq ? num_selected : max_blocks_per_seq;
+        const long long units = (long long)num_seqs * (num_kv_heads / HG) * width;
+        if (units > 0 && runs > (units + 3) / 4)
+            runs = (int)((units + 3) / 4);
     }
     DecodeParams p;
     const int st = decode_prepare(out, q, k_cache, v_cache, block_tables, seq_lens, num_seqs, num_heads, num_kv_heads,

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import paged_kv_cache_462_b200 as pkv
-from test_binding_cpu import FakeLib, Stream, cuda
+from test_binding_cpu import FakeLib, cuda
 
 P = 0x100000        # never dereferenced: the calls below fail a host check first, or have nothing to do
 FAR = 0x40000000
@@ -162,7 +162,7 @@ def fake(monkeypatch):
     f = FakeLib()
     monkeypatch.setattr(pkv, "load_library", lambda: f)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a, **k: Stream(0))
+    monkeypatch.setattr(pkv, "_current_raw_stream", lambda dev: 7)
     return f
 
 
@@ -184,7 +184,7 @@ def test_norm_rope_argument_order(fake):
     pkv.qk_norm_rope_and_cache(**x, interleaved=True, k_scale=2.0, v_scale=3.0)
     name, a = fake.calls[-1]
     assert name == "qk_norm_rope_and_cache"
-    assert a[1].value == x["q"].data_ptr() and a[3].value == x["v"].data_ptr()
+    assert a[1] == x["q"].data_ptr() and a[3] == x["v"].data_ptr() and a[-1] == 7
     assert a[12:21] == (3, 8, 2, 64, 32, 10, 16, 4, 1)
     assert a[21:24] == (768, 768, 768)                    # the projection's row, in elements
     assert a[24:28] == (pkv.BF16, pkv.BF16, 2.0, 3.0)
@@ -242,11 +242,11 @@ def test_decode_bindings(fake):
     pkv.paged_attention_decode_block_scales(**x, k_block_scales=ks, v_block_scales=vs, num_partitions=7)
     name, a = fake.calls.pop()
     assert a[6:16] == (3, 8, 2, 128, 16, 0.5, 6, 4, pkv.BF16, pkv.FP8_E4M3) and a[18] == 7
-    assert (a[16].value, a[17].value) == (ks.data_ptr(), vs.data_ptr())
+    assert (a[16], a[17]) == (ks.data_ptr(), vs.data_ptr())
     pkv.paged_attention_decode_sparse(**x, selected=i32(3, 2, 5), k_scale=2.0, v_scale=3.0)
     name, a = fake.calls.pop()
     assert a[7:20] == (3, 8, 2, 128, 16, 0.5, 6, 4, 5, pkv.BF16, pkv.FP8_E4M3, 2.0, 3.0)
-    assert a[20].value is None and a[21].value is None
+    assert a[20] is None and a[21] is None
     for bad in (dict(selected=i32(3, 4, 5)), dict(selected=cuda(torch.zeros(3, 2, 5, dtype=torch.int64)))):
         with pytest.raises(TypeError):
             pkv.paged_attention_decode_sparse(**x, **bad)
@@ -261,7 +261,7 @@ def test_select_bindings(fake):
     kb = bf(4, 2, 2, 128)
     pkv.update_key_bounds(kb, bf(4, 2, 16, 128), i32(3, 6), i32(3), i32(4), 9)
     name, a = fake.calls.pop()
-    assert a[5:14] == (9, 3, 2, 128, 16, 6, 4, pkv.BF16, 1.0) and a[14].value is None
+    assert a[5:14] == (9, 3, 2, 128, 16, 6, 4, pkv.BF16, 1.0) and a[14] is None
     with pytest.raises(TypeError):
         pkv.update_key_bounds(bf(4, 2, 128, 2), bf(4, 2, 16, 128), i32(3, 6), i32(3), i32(4), 9)
     x = dict(selected=i32(3, 2, 5), q=bf(3, 8, 128), key_bounds=kb, block_tables=i32(3, 6), seq_lens=i32(3),
