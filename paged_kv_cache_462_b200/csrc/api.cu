@@ -146,6 +146,16 @@ bool ensure_smem_attribute(const void* kernel, size_t bytes)
     return true;
 }
 
+bool recorded(cudaStream_t stream)
+{
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &status) != cudaSuccess) {
+        (void)cudaGetLastError();   // the legacy stream while another one captures: not recorded
+        return false;
+    }
+    return status != cudaStreamCaptureStatusNone;
+}
+
 // Host checks, partition count and launch parameters of a decode call; nothing is queued. On
 // PKV_OK, *runs = 0 means there is nothing to launch (no sequences).
 int decode_prepare(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
@@ -388,21 +398,10 @@ int decode_impl(void* out, const void* q, const void* k_cache, const void* v_cac
                                   q_len, k_head_scales, v_head_scales, &p, &runs);
     if (st != PKV_OK || runs == 0)
         return st;
+    if (recorded(static_cast<cudaStream_t>(stream)))
+        p.chunk_done = nullptr;
     return decode_dispatch(q_dtype, kv_dtype, head_dim, block_size, num_heads / num_kv_heads * q_len, p, runs,
                            static_cast<cudaStream_t>(stream), nullptr);
-}
-
-// A launch on `stream` is being recorded into a graph. A replay repeats the recorded parameters,
-// the call's epoch among them, so that a chunk's stamp of the replay before would pass for its own:
-// a recorded merge waits for the whole decode grid instead of the stamps.
-bool recorded(cudaStream_t stream)
-{
-    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream, &status) != cudaSuccess) {
-        (void)cudaGetLastError();   // the legacy stream while another one captures: not recorded
-        return false;
-    }
-    return status != cudaStreamCaptureStatusNone;
 }
 
 // The decodes whose producer resolves every KV head for itself: over selected blocks, over a cache

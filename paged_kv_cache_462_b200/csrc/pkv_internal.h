@@ -168,6 +168,11 @@ int decode_prepare(void* out, const void* q, const void* k_cache, const void* v_
                    const AppendArgs* app, int withheld_unit, int q_len, const float* k_head_scales,
                    const float* v_head_scales, DecodeParams* p_out, int* runs);
 
+// Whether launches on `stream` are being recorded into a graph. A replay repeats the recorded
+// parameters, the call's epoch among them, so that a chunk's stamp of the replay before would pass
+// for its own: a recorded call goes without stamps (chunk_done null), its merge waits for the grid.
+bool recorded(cudaStream_t stream);
+
 // Raise a kernel's dynamic shared-memory limit to at least `bytes` on the current device (cached).
 bool ensure_smem_attribute(const void* kernel, size_t bytes);
 

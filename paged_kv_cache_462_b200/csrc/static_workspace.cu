@@ -125,6 +125,8 @@ extern "C" PKV_API int paged_attention_decode_static(
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (cudaMemsetAsync(ws, 0, zero_bytes < need ? zero_bytes : need, s) != cudaSuccess)
         return PKV_ERR_LAUNCH;
+    if (pkv::recorded(s))
+        p.chunk_done = nullptr;
     return pkv::decode_dispatch(q_dtype, kv_dtype, head_dim, block_size, num_heads / num_kv_heads, p, runs, s,
                                 nullptr);
 }
