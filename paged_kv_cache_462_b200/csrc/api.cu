@@ -428,6 +428,8 @@ int heads_impl(void* out, const void* q, const void* k_cache, const void* v_cach
         return PKV_ERR_SHAPE;
     if (num_seqs == 0)
         return PKV_OK;
+    if (!aligned16(q))   // read in pieces of up to 8 bytes
+        return PKV_ERR_SHAPE;
     int runs = num_partitions;
     const int HG = mma_head_group(kv_dtype, head_dim, block_size, num_kv_heads);
     MmaOp op{};

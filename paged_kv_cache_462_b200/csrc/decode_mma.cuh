@@ -614,8 +614,10 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
                             atomicOr(p.err, PKV_DEVERR_SELECTION);
                         if (j[w] < 0 || j[w] >= blocks)
                             j[w] = -1;
-                        else
+                        else if (p.selected != nullptr || w == 0)   // (all blocks: one for all heads)
                             u.row[w] = __ldg(p.block_tables + (long long)s * p.max_blocks_per_seq + j[w]);
+                        else
+                            u.row[w] = u.row[0];
                     }
 #pragma unroll
                     for (int w = 0; w < HG; ++w) {
@@ -693,7 +695,16 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
                         }
                         issued = k + 1;
                         __syncwarp();
-                        if (row >= 0) {   // one box of block_size rows per 128 bytes of the head's tile
+                        if (p.selected == nullptr) {   // the heads' tiles are one run: boxes of all of them
+                            if (lane == 0 && row >= 0) {
+#pragma unroll
+                                for (int bx = 0; bx < C::kBoxes; ++bx) {
+                                    uint8_t* at = dst + bx * C::kBoxBytes;
+                                    tma_load_2d(at, &kmap, bx * C::kBoxCols, row, &full[st]);
+                                    tma_load_2d(at + C::kHalf, &vmap, bx * C::kBoxCols, row, &full[st]);
+                                }
+                            }
+                        } else if (row >= 0) {   // one box of block_size rows per 128 bytes of the head's tile
 #pragma unroll
                             for (int bx = 0; bx < C::kBoxes; ++bx) {
                                 uint8_t* at = dst + bx * C::kBoxBytes + lane * (BS * 128);
@@ -1604,7 +1615,7 @@ struct MmaLauncher {
         if constexpr (KV::kBytes == 1)
             kvdt = KV::kInt8 ? PKV_INT8 : KV::kFmt == __NV_E5M2 ? PKV_FP8_E5M2 : PKV_FP8_E4M3;
         CUtensorMap kmap, vmap;
-        const int box_rows = PH ? BS : C::kRows;   // PH: one head's rows at a time
+        const int box_rows = PH && p.selected != nullptr ? BS : C::kRows;   // selected: a head's rows at a time
         if (!make_cache_tensormap(&kmap, p.k_cache, kvdt, D, rows, box_rows) ||
             !make_cache_tensormap(&vmap, p.v_cache, kvdt, D, rows, box_rows))
             return PKV_ERR_LAUNCH;

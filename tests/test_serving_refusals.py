@@ -97,7 +97,7 @@ def decode(lib, sparse, **kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(S=-1), SHAPE), (dict(Hq=6, Hkv=2), SHAPE), (dict(Hq=7), SHAPE), (dict(D=64), SHAPE), (dict(BS=8), SHAPE),
     (dict(qd=0), DTYPE), (dict(kv=0), DTYPE), (dict(parts=-1), SHAPE), (dict(o=None), NULL), (dict(sl=None), NULL),
-    (dict(kc=P + 8), SHAPE), (dict(ws=None), WS), (dict(wsb=1024), WS), (dict(MB=0), SHAPE), (dict(NB=0), SHAPE),
+    (dict(kc=P + 8), SHAPE), (dict(q=P + 8), SHAPE), (dict(ws=None), WS), (dict(wsb=1024), WS), (dict(MB=0), SHAPE), (dict(NB=0), SHAPE),
     (dict(vb=None), NULL), (dict(S=0, o=None), 0)])
 def test_decode_refusals(lib, sparse, kw, want):
     assert decode(lib, sparse, **kw) == want
