@@ -25,8 +25,9 @@
 // memory, so a producer warp brings 16 blocks (or a few times 16) of up to four heads at a time into
 // a ring of shared-memory stages by bulk copies, and a warp per head and 16 blocks turns them into
 // scores. Two CTAs an SM share all stages of the batch evenly, each a range of them. The second,
-// queued behind it as a dependent launch, selects, a CTA per stream: up to 2048 blocks are kept in
-// registers, eight a thread, with as few exchanges as the steps allow (latency is all it costs).
+// queued behind it as a dependent launch, selects, a CTA per stream: up to 2048 blocks (or 16384, with
+// four times the threads) are kept in registers, with as few exchanges as the steps allow: latency is
+// all it costs.
 #include <cstdint>
 
 #include "device.cuh"
@@ -40,10 +41,11 @@ constexpr int kScoreWarps = 4;                // consumer warps, each a KV head'
 constexpr int kScoreThreads = (kScoreWarps + 1) * 32;
 constexpr int kScoreStages = 3;
 constexpr int kRowPad = 64;                   // bytes behind a block's run: neighbouring rows meet other banks
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelPerThread = 8;              // keys a thread holds: streams of up to 2048 blocks
-constexpr int kSelSmemKeys = 8192;            // longer ones are selected in shared memory up to this many
+// selection: threads of a CTA and keys a thread holds, for tables of up to 2048 blocks and for wider ones
+constexpr int kSelThreads = 256, kSelPerThread = 8;
+constexpr int kSelWideThreads = 1024, kSelWidePerThread = 16;
+constexpr int kSelNear = 256;                 // blocks near the border that are ranked in shared memory
+constexpr int kSelSmemKeys = 4096;            // what registers cannot settle is selected in shared memory up to this many
 constexpr float kSelError = 7.62939453125e-06f;   // 2^-17
 constexpr uint32_t kChosen = 0xffffffffu;
 
@@ -106,6 +108,7 @@ __device__ __forceinline__ unsigned long long sort_key(double f)
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
+template <int NW>
 __device__ __forceinline__ int block_sum(int v, int* scratch)
 {
 #pragma unroll
@@ -117,12 +120,13 @@ __device__ __forceinline__ int block_sum(int v, int* scratch)
     __syncthreads();
     int s = 0;
 #pragma unroll
-    for (int i = 0; i < kSelWarps; ++i)
+    for (int i = 0; i < NW; ++i)
         s += scratch[i];
     return s;
 }
 
 // Both sums in one exchange.
+template <int NW>
 __device__ __forceinline__ void block_sum2(int& a, int& b, int2* scratch)
 {
 #pragma unroll
@@ -136,13 +140,14 @@ __device__ __forceinline__ void block_sum2(int& a, int& b, int2* scratch)
     __syncthreads();
     a = b = 0;
 #pragma unroll
-    for (int i = 0; i < kSelWarps; ++i) {
+    for (int i = 0; i < NW; ++i) {
         a += scratch[i].x;
         b += scratch[i].y;
     }
 }
 
 // Exclusive sum over the CTA's threads in order; `total` the sum of all.
+template <int NW>
 __device__ __forceinline__ int block_scan(int v, int* scratch, int& total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -160,7 +165,7 @@ __device__ __forceinline__ int block_scan(int v, int* scratch, int& total)
     int base = 0;
     total = 0;
 #pragma unroll
-    for (int i = 0; i < kSelWarps; ++i) {
+    for (int i = 0; i < NW; ++i) {
         if (i < warp)
             base += scratch[i];
         total += scratch[i];
@@ -497,28 +502,28 @@ __device__ __forceinline__ double near_score_of(const SelectArgs& p, const __nv_
     return exact_score<D, G>(q, p.bounds + tile * (2 * D), lane);
 }
 
+template <int NT, int K>
 struct FastShared {
     int hist[4][256];
     int taken[4];                        // keys gathered after each pass; [3]: near blocks
     uint32_t list[32];
-    uint32_t reduce[3][kSelWarps];
-    int above[kSelWarps];
-    int near_block[kSelThreads];
-    uint32_t near_key[kSelThreads];
-    unsigned long long near_val[kSelThreads];
-    uint32_t chosen[kSelThreads * kSelPerThread / 32];
-    int counts[kSelPerThread * kSelWarps];
+    uint32_t reduce[3][NT / 32];
+    int above[NT / 32];
+    int near_block[kSelNear];
+    uint32_t near_key[kSelNear];
+    unsigned long long near_val[kSelNear];
+    uint32_t chosen[NT * K / 32];
+    int counts[NT / 32 * K];
 };
 
-// Selection among up to kSelThreads * kSelPerThread blocks by the CTA; thread t holds the keys of blocks
-// t, t + 256, ... Returns false, having written nothing, if more blocks than threads are too close to
-// the border.
-template <int D, int G>
+// Selection among up to NT * K blocks by the CTA; thread t holds the keys of blocks t, t + NT, ...
+// Returns false, having written nothing, if more than kSelNear blocks are too close to the border.
+template <int D, int G, int NT, int K>
 __device__ __forceinline__ bool select_in_registers(const SelectArgs& p, const __nv_bfloat16* q, const int32_t* table,
                                                     const float* scores, const float* magnitude, int nb, int h,
-                                                    int32_t* out, FastShared& sh)
+                                                    int32_t* out, FastShared<NT, K>& sh)
 {
-    constexpr int K = kSelPerThread;
+    constexpr int NW = NT / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int need = p.keep - p.sink - p.recent;
     uint32_t keys[K];
@@ -526,22 +531,21 @@ __device__ __forceinline__ bool select_in_registers(const SelectArgs& p, const _
     float mag = 0.f;
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-        const int j = i * kSelThreads + tid;
+        const int j = i * NT + tid;
         score[i] = j < nb ? __ldcg(scores + j) : 0.f;
     }
-    for (int i = tid; i < (nb + 15) / 16; i += kSelThreads)
+    for (int i = tid; i < (nb + 15) / 16; i += NT)
         mag = fmaxf(mag, __ldcg(magnitude + i));
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        sh.hist[i][tid] = 0;
+    for (int i = tid; i < 4 * 256; i += NT)
+        sh.hist[i / 256][i % 256] = 0;
     if (tid < 4)
         sh.taken[tid] = 0;
-    if (tid < kSelThreads * K / 32)
-        sh.chosen[tid] = 0u;
+    for (int i = tid; i < NT * K / 32; i += NT)
+        sh.chosen[i] = 0u;
     uint32_t kmin = 0xffffffffu, kmax = 0u;
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-        const int j = i * kSelThreads + tid;
+        const int j = i * NT + tid;
         keys[i] = j < nb ? sort_key(score[i]) : 0u;      // behind the last block: below every key
         if (j < p.sink || (j < nb && j >= nb - p.recent)) {
             keys[i] = kChosen;
@@ -561,7 +565,7 @@ __device__ __forceinline__ bool select_in_registers(const SelectArgs& p, const _
     __syncthreads();
     uint32_t mbits = 0u;
 #pragma unroll
-    for (int i = 0; i < kSelWarps; ++i) {
+    for (int i = 0; i < NW; ++i) {
         kmin = min(kmin, sh.reduce[0][i]);
         kmax = max(kmax, sh.reduce[1][i]);
         mbits = max(mbits, sh.reduce[2][i]);
@@ -645,8 +649,8 @@ __device__ __forceinline__ bool select_in_registers(const SelectArgs& p, const _
             above += keys[i] > up && keys[i] != kChosen;
             if (keys[i] >= down && keys[i] <= up) {
                 const int at = atomicAdd(&sh.taken[3], 1);
-                if (at < kSelThreads) {
-                    sh.near_block[at] = i * kSelThreads + tid;
+                if (at < kSelNear) {
+                    sh.near_block[at] = i * NT + tid;
                     sh.near_key[at] = keys[i];
                 }
             }
@@ -658,14 +662,14 @@ __device__ __forceinline__ bool select_in_registers(const SelectArgs& p, const _
         const int near = sh.taken[3];
         int want = need;                 // of the near ones; 1 <= want <= near
 #pragma unroll
-        for (int i = 0; i < kSelWarps; ++i)
+        for (int i = 0; i < NW; ++i)
             want -= sh.above[i];
         take = down;
         if (want < near) {
-            if (near > kSelThreads)
+            if (near > kSelNear)
                 return false;
             take = up + 1u;
-            for (int i = warp; i < near; i += kSelWarps) {
+            for (int i = warp; i < near; i += NW) {
                 const double v = near_score_of<D, G>(p, q, table, h, sh.near_block[i], sh.near_key[i], lane);
                 if (lane == 0)
                     sh.near_val[i] = sort_key(v);
@@ -685,7 +689,7 @@ __device__ __forceinline__ bool select_in_registers(const SelectArgs& p, const _
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < K; ++i)
-                if (sh.chosen[i * (kSelThreads / 32) + warp] >> lane & 1u)
+                if (sh.chosen[i * NW + warp] >> lane & 1u)
                     keys[i] = kChosen;
         }
     }
@@ -695,37 +699,50 @@ __device__ __forceinline__ bool select_in_registers(const SelectArgs& p, const _
     for (int i = 0; i < K; ++i) {
         m[i] = __ballot_sync(kFullMask, keys[i] >= take);
         if (lane == 0)
-            sh.counts[i * kSelWarps + warp] = __popc(m[i]);
+            sh.counts[i * NW + warp] = __popc(m[i]);
     }
     __syncthreads();
-    const int c0 = sh.counts[2 * lane], c1 = sh.counts[2 * lane + 1];
-    int upto = c0 + c1;
+    if (warp == 0) {                     // what comes before each of them, K * NW / 32 a lane
+        constexpr int E = K * NW / 32;
+        int c[E], sum = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(kFullMask, upto, o);
-        if (lane >= o)
-            upto += y;
+        for (int e = 0; e < E; ++e) {
+            c[e] = sh.counts[lane * E + e];
+            sum += c[e];
+        }
+        int before = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFullMask, before, o);
+            if (lane >= o)
+                before += y;
+        }
+        before -= sum;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            sh.counts[lane * E + e] = before;
+            before += c[e];
+        }
     }
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-        const int e = i * kSelWarps + warp;      // entries before this warp's, two a lane
-        const int upto_pair = __shfl_sync(kFullMask, upto, e / 2);
-        const int pair0 = __shfl_sync(kFullMask, c0, e / 2), pair1 = __shfl_sync(kFullMask, c1, e / 2);
-        const int at = upto_pair - pair1 - (e & 1 ? 0 : pair0) + __popc(m[i] & ((1u << lane) - 1u));
+        const int at = sh.counts[i * NW + warp] + __popc(m[i] & ((1u << lane) - 1u));
         if ((m[i] >> lane & 1u) && at < p.keep)
-            out[at] = i * kSelThreads + tid;
+            out[at] = i * NT + tid;
     }
     return true;
 }
 
-template <int D, int G>
-__global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const SelectArgs p)
+template <int D, int G, int NT, int K>
+__global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs p)
 {
+    constexpr int NW = NT / 32;
     extern __shared__ uint32_t smem_keys[];
-    __shared__ int scratch[kSelWarps];
-    __shared__ int2 scratch2[kSelWarps];
-    __shared__ double near_vals[kSelThreads];
-    __shared__ float fscratch[kSelWarps];
+    __shared__ int scratch[NW];
+    __shared__ int2 scratch2[NW];
+    __shared__ double near_vals[kSelNear];
+    __shared__ float fscratch[NW];
     __shared__ int hist[256];
     __shared__ int bcast[3];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -735,7 +752,7 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
     // (the scoring grid may still run; the next call's waits for this one's end)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (nb <= p.keep) {                  // everything is kept
-        for (int i = tid; i < p.keep; i += kSelThreads)
+        for (int i = tid; i < p.keep; i += NT)
             out[i] = i < nb ? i : -1;
         return;
     }
@@ -743,17 +760,17 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
     const int32_t* table = p.block_tables + (long long)s * p.max_blocks;
     float* scores = p.scores + (long long)stream * p.max_blocks;
     const float* magnitude = p.magnitude + (long long)stream * p.runs;
-    __shared__ FastShared fast;
-    if (nb <= kSelThreads * kSelPerThread && select_in_registers<D, G>(p, q, table, scores, magnitude, nb, h, out, fast))
+    __shared__ FastShared<NT, K> fast;
+    if (nb <= NT * K && select_in_registers<D, G, NT, K>(p, q, table, scores, magnitude, nb, h, out, fast))
         return;
     const bool in_smem = nb <= kSelSmemKeys;
     uint32_t* keys = in_smem ? smem_keys : reinterpret_cast<uint32_t*>(scores);
     const int need = p.keep - p.sink - p.recent;   // among blocks [sink, nb - recent), more than `need` of them
     float mag = 0.f;
-    for (int i = tid; i < (nb + 15) / 16; i += kSelThreads)
+    for (int i = tid; i < (nb + 15) / 16; i += NT)
         mag = fmaxf(mag, __ldcg(magnitude + i));
     uint32_t kmin = 0xffffffffu, kmax = 0u;
-    for (int j = tid; j < nb; j += kSelThreads) {
+    for (int j = tid; j < nb; j += NT) {
         uint32_t k = sort_key(__ldcg(scores + j));
         if (j < p.sink || j >= nb - p.recent) {
             k = kChosen;
@@ -769,7 +786,7 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
         kmin = min(kmin, __shfl_xor_sync(kFullMask, kmin, o));
         kmax = max(kmax, __shfl_xor_sync(kFullMask, kmax, o));
     }
-    __shared__ uint32_t range[2][kSelWarps];
+    __shared__ uint32_t range[2][NW];
     if (lane == 0) {
         range[0][warp] = kmin;
         range[1][warp] = kmax;
@@ -777,7 +794,7 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kSelWarps; ++i) {
+    for (int i = 0; i < NW; ++i) {
         kmin = min(kmin, range[0][i]);
         kmax = max(kmax, range[1][i]);
         mag = fmaxf(mag, fscratch[i]);
@@ -785,16 +802,17 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
 
     if (need > 0) {
         // the key of the need-th largest: 256 equal bins between the smallest and the largest key
-        // left, then the same within the bin it lies in, until that holds at most one key a thread
+        // left, then the same within the bin it lies in, until that holds at most 256
         uint32_t lo = kmin, hi = kmax;
         int rank = need;                 // the rank-th largest of the keys in [lo, hi]
         int in_bin = nb;
-        for (int pass = 0; pass < 5 && lo < hi && in_bin > kSelThreads; ++pass) {
+        for (int pass = 0; pass < 5 && lo < hi && in_bin > 256; ++pass) {
             const uint32_t span = hi - lo;
             const int shift = span < 256u ? 0 : 24 - __clz(span);
-            hist[tid] = 0;
+            if (tid < 256)
+                hist[tid] = 0;
             __syncthreads();
-            for (int j = tid; j < nb; j += kSelThreads) {
+            for (int j = tid; j < nb; j += NT) {
                 const uint32_t k = keys[j];
                 if (k >= lo && k <= hi)
                     atomicAdd(&hist[(k - lo) >> shift], 1);
@@ -802,8 +820,8 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
             __syncthreads();
             int total;
             // thread i holds bin 255 - i: how many keys lie in higher bins
-            const int mine = hist[255 - tid];
-            const int above = block_scan(mine, scratch, total);
+            const int mine = tid < 256 ? hist[255 - tid] : 0;
+            const int above = block_scan<NW>(mine, scratch, total);
             if (mine > 0 && above < rank && rank <= above + mine) {
                 bcast[0] = 255 - tid;
                 bcast[1] = rank - above;
@@ -823,16 +841,16 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
             if (tid == 0)
                 bcast[0] = 0;
             __syncthreads();
-            for (int j = tid; j < nb; j += kSelThreads) {
+            for (int j = tid; j < nb; j += NT) {
                 const uint32_t k = keys[j];
                 if (k >= lo && k <= hi) {
                     const int at = atomicAdd(&bcast[0], 1);
-                    if (at < kSelThreads)
+                    if (at < 256)
                         hist[at] = (int)k;
                 }
             }
             __syncthreads();
-            const int n = min(bcast[0], kSelThreads);
+            const int n = min(bcast[0], 256);
             if (tid < n) {
                 const uint32_t k = (uint32_t)hist[tid];
                 int greater = 0, equal = 0;
@@ -850,12 +868,12 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
         uint32_t down, up;
         border_zone(lo, mag, down, up);
         int above = 0, near = 0;
-        for (int j = tid; j < nb; j += kSelThreads) {
+        for (int j = tid; j < nb; j += NT) {
             const uint32_t k = keys[j];
             above += k > up && k != kChosen;
             near += k >= down && k <= up;
         }
-        block_sum2(above, near, scratch2);
+        block_sum2<NW>(above, near, scratch2);
         int want = need - above;         // of the `near` ones; 1 <= want <= near
         const bool all = want == near;
         uint32_t take = all ? down : up + 1u;        // keys from here on are chosen
@@ -863,23 +881,23 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
             int32_t* list = p.near_list + (long long)stream * p.max_blocks;
             double* val = p.near_score + (long long)stream * p.max_blocks;
             // the near blocks in ascending order
-            const int seg = (nb + kSelThreads - 1) / kSelThreads;
+            const int seg = (nb + NT - 1) / NT;
             const int b = min(nb, tid * seg), e = min(nb, b + seg);
             int cnt = 0, total;
             for (int j = b; j < e; ++j)
                 cnt += keys[j] >= down && keys[j] <= up;
-            int at = block_scan(cnt, scratch, total);
+            int at = block_scan<NW>(cnt, scratch, total);
             for (int j = b; j < e; ++j)
                 if (keys[j] >= down && keys[j] <= up)
                     list[at++] = j;
             __syncthreads();
-            for (int i = warp; i < near; i += kSelWarps) {
+            for (int i = warp; i < near; i += NW) {
                 const double v = near_score_of<D, G>(p, q, table, h, list[i], keys[list[i]], lane);
                 if (lane == 0)
-                    (near <= kSelThreads ? near_vals : val)[i] = v;
+                    (near <= kSelNear ? near_vals : val)[i] = v;
             }
             __syncthreads();
-            if (near <= kSelThreads) {   // a few: each is ranked against the others, ties by index
+            if (near <= kSelNear) {   // a few: each is ranked against the others, ties by index
                 if (tid < near) {
                     const unsigned long long mine = sort_key(near_vals[tid]);
                     int better = 0;
@@ -896,22 +914,22 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
                 for (int bit = 63; bit >= 0; --bit) {
                     const unsigned long long trial = bound | (1ull << bit);
                     int c = 0;
-                    for (int i = tid; i < near; i += kSelThreads)
+                    for (int i = tid; i < near; i += NT)
                         c += sort_key(val[i]) >= trial;
-                    if (block_sum(c, scratch) >= want)
+                    if (block_sum<NW>(c, scratch) >= want)
                         bound = trial;
                 }
                 int more = 0;
-                for (int i = tid; i < near; i += kSelThreads)
+                for (int i = tid; i < near; i += NT)
                     more += sort_key(val[i]) > bound;
-                more = block_sum(more, scratch);
+                more = block_sum<NW>(more, scratch);
                 want -= more;                // of the ties, in order
-                const int seg2 = (near + kSelThreads - 1) / kSelThreads;
+                const int seg2 = (near + NT - 1) / NT;
                 const int b2 = min(near, tid * seg2), e2 = min(near, b2 + seg2);
                 int ties = 0;
                 for (int i = b2; i < e2; ++i)
                     ties += sort_key(val[i]) == bound;
-                int rank2 = block_scan(ties, scratch, total);
+                int rank2 = block_scan<NW>(ties, scratch, total);
                 for (int i = b2; i < e2; ++i) {
                     const unsigned long long k = sort_key(val[i]);
                     const bool chosen = k > bound || (k == bound && rank2 < want);
@@ -922,17 +940,17 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
             }
         }
         // emit in ascending order: chosen keys and those from `take` on
-        const int seg = (nb + kSelThreads - 1) / kSelThreads;
+        const int seg = (nb + NT - 1) / NT;
         const int b = min(nb, tid * seg), e = min(nb, b + seg);
         int cnt = 0, total;
         for (int j = b; j < e; ++j)
             cnt += keys[j] >= take;
-        int at = block_scan(cnt, scratch, total);
+        int at = block_scan<NW>(cnt, scratch, total);
         for (int j = b; j < e; ++j)
             if (keys[j] >= take && at < p.keep)
                 out[at++] = j;
     } else {
-        for (int i = tid; i < p.keep; i += kSelThreads)
+        for (int i = tid; i < p.keep; i += NT)
             out[i] = i < p.sink ? i : nb - p.keep + i;
     }
 }
@@ -965,7 +983,6 @@ template <int D, int G>
 int launch_select(SelectArgs p, int num_seqs, cudaStream_t stream)
 {
     auto score = score_blocks_kernel<D, G>;
-    auto select = select_blocks_kernel<D, G>;
     p.heads = p.num_kv_heads < kScoreWarps ? p.num_kv_heads : kScoreWarps;
     p.head_groups = (p.num_kv_heads + p.heads - 1) / p.heads;
     p.tiles = kScoreWarps / p.heads;
@@ -981,9 +998,12 @@ int launch_select(SelectArgs p, int num_seqs, cudaStream_t stream)
     score<<<grid, kScoreThreads, smem, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess)
         return PKV_ERR_LAUNCH;
+    const bool wide = p.max_blocks > kSelThreads * kSelPerThread;
+    auto select = wide ? select_blocks_kernel<D, G, kSelWideThreads, kSelWidePerThread>
+                       : select_blocks_kernel<D, G, kSelThreads, kSelPerThread>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(num_seqs * p.num_kv_heads));
-    cfg.blockDim = dim3(kSelThreads);
+    cfg.blockDim = dim3(wide ? kSelWideThreads : kSelThreads);
     cfg.dynamicSmemBytes = (size_t)(p.max_blocks < kSelSmemKeys ? p.max_blocks : kSelSmemKeys) * 4;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

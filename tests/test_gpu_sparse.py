@@ -142,9 +142,9 @@ def test_select_scores_that_fp32_cannot_tell_apart():
     check_select([16 * n], 2, 1, D, 16, 333, 0, 3, q=q.to(torch.bfloat16), b=b)
 
 
-@pytest.mark.parametrize("blocks", [8192, 8193, 20001])
+@pytest.mark.parametrize("blocks", [2048, 2049, 8192, 8193, 16384, 16385, 20001])
 def test_select_long_sequences(blocks):
-    """Around and beyond the streams that are selected in shared memory."""
+    """Around and beyond the streams that are selected in registers."""
     check_select([16 * blocks - 5], 4, 1, 64, 16, 100)
     check_select([16 * blocks], 4, 1, 64, 16, 700, 0, 0, step=4.0, seed=2)
 
