@@ -376,3 +376,145 @@ def test_steps_of_a_server(cache):
         short = [s for s, L in enumerate(have) if L <= keep * block]
         assert short and float((out[short].float() - dense[short].float()).abs().max()) <= 2.0 ** -7 * float(dense.float().abs().max())
     assert err.item() == 0
+
+
+def test_far_blocks():
+    """Blocks beyond 2^31 elements of the caches: appended, bounded, selected and attended like near ones."""
+    S, Hq, Hkv, D, block = 2, 8, 8, 128, 16
+    NB = 140000                                            # 2.29e9 elements a cache
+    lens = [75, 200]
+    gen = torch.Generator().manual_seed(21)
+    n = [-(-L // block) for L in lens]
+    table = torch.full((S, max(n)), -1, dtype=torch.int32)
+    far = NB - 1 - torch.arange(sum(n), dtype=torch.int32)
+    for s in range(S):
+        table[s, :n[s]] = far[sum(n[:s]):sum(n[:s + 1])]
+    near = torch.where(table >= 0, NB - 1 - table, table)   # the same blocks at the pool's start
+    T = sum(lens)
+    k, v = (torch.randn(T, Hkv, D, generator=gen).to(torch.bfloat16).cuda() for _ in range(2))
+    q = torch.randn(S, Hq, D, generator=gen).to(torch.bfloat16).cuda()
+    sl = torch.tensor(lens, dtype=torch.int32).cuda()
+    ro = torch.tensor([0, lens[0], T], dtype=torch.int32).cuda()
+    res = []
+    for t, pool in ((table, NB), (near, sum(n))):
+        dt = t.cuda()
+        kc = torch.zeros(pool, Hkv, block, D, dtype=torch.float8_e4m3fn, device="cuda")
+        vc = torch.zeros_like(kc)
+        ks, vs = torch.zeros(pool, Hkv, device="cuda"), torch.zeros(pool, Hkv, device="cuda")
+        kb = torch.zeros(pool, Hkv, 2, D, dtype=torch.bfloat16, device="cuda")
+        sel = torch.empty(S, Hkv, 4, dtype=torch.int32, device="cuda")
+        o1, o2 = torch.empty_like(q), torch.empty_like(q)
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        pkv.reshape_and_cache_block_scales(k, v, kc, vc, ks, vs, dt, sl, ro, device_error=err)
+        pkv.update_key_bounds(kb, kc, dt, sl, ro, T, k_block_scales=ks, device_error=err)
+        pkv.select_blocks(sel, q, kb, dt, sl, block)
+        pkv.paged_attention_decode_sparse(o1, q, kc, vc, dt, sl, sel, 0.1, k_block_scales=ks, v_block_scales=vs, num_partitions=4)
+        pkv.paged_attention_decode_block_scales(o2, q, kc, vc, dt, sl, 0.1, ks, vs, num_partitions=4)
+        # and the fused norm + append into a bf16 pool of that many blocks, one row in the last block
+        kc16 = torch.zeros(pool, Hkv, block, D, dtype=torch.bfloat16, device="cuda")
+        vc16 = torch.zeros_like(kc16)
+        w = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+        slot = torch.tensor([(pool - 1 if pool == NB else 0) * block + 3], device="cuda")
+        pkv.qk_norm_rope_and_cache(torch.empty_like(q[:1]), q[:1], k[:1], v[:1], w, w, 1e-6,
+                                   torch.ones(1, D, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda"),
+                                   kc16, vc16, slot, device_error=err)
+        assert err.item() == 0
+        at = t[t >= 0].long().cuda()
+        b = int(slot) // block
+        res.append([x.clone() for x in (kc.view(torch.uint8)[at], vc.view(torch.uint8)[at], ks[at], vs[at], kb[at], sel,
+                                        o1, o2, kc16[b], vc16[b])])
+        del kc, vc, kc16, vc16, kb
+    torch.cuda.empty_cache()
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+    assert bool(res[0][8].any())
+
+
+def test_two_streams_at_once():
+    """Selection and sparse decode on two streams at the same time, without workspaces of their own."""
+    gen = torch.Generator().manual_seed(31)
+    lens = [3000, 700, 1999, 40, 2500, 16]
+    table, pool = plain.tables(lens, 16, gen)
+    b = bounds_like(pool, 2, 128, gen).cuda()
+    k, v = (torch.randn(pool, 2, 16, 128, generator=gen).to(torch.bfloat16).cuda() for _ in range(2))
+    dt, sl = table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    qs = [torch.randn(6, 8, 128, generator=gen).to(torch.bfloat16).cuda() for _ in range(2)]
+
+    def run(q):
+        sel = torch.empty(6, 2, 24, dtype=torch.int32, device="cuda")
+        out = torch.empty_like(q)
+        pkv.select_blocks(sel, q, b, dt, sl, 16)
+        pkv.paged_attention_decode_sparse(out, q, k, v, dt, sl, sel, 0.1)
+        return sel, out
+
+    want = [run(q) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(run(qs[i]))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for x in g:
+            assert torch.equal(x[0], w[0]) and torch.equal(x[1], w[1])
+
+
+def test_a_step_captured_and_replayed():
+    """Norm, append, bounds, selection and attention in one graph, replayed with other queries and
+    lengths: the same as the calls made one by one."""
+    S, Hq, Hkv, D, block, keep = 3, 8, 2, 128, 16, 6
+    gen = torch.Generator().manual_seed(41)
+    final = [400, 130, 260]
+    table, pool = plain.tables(final, block, gen)
+    dt = table.cuda()
+    cs = torch.randn(512, D, generator=gen).cuda()
+    w = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    ro = torch.arange(S + 1, dtype=torch.int32, device="cuda")
+
+    class Run:
+        def __init__(self):
+            g = torch.Generator(device="cuda").manual_seed(5)
+            code = lambda: (torch.randn(pool, Hkv, block, D, generator=g, device="cuda") * 60).to(torch.float8_e4m3fn)
+            self.kc, self.vc = code(), code()
+            self.ks = torch.full((pool, Hkv), 2.0 ** -6, device="cuda")
+            self.vs = self.ks.clone()
+            self.kb = torch.zeros(pool, Hkv, 2, D, dtype=torch.bfloat16, device="cuda")
+            self.sl = torch.tensor([f - 8 for f in final], dtype=torch.int32, device="cuda")
+            pkv.update_key_bounds(self.kb, self.kc, dt, self.sl, torch.cat([ro[:1], self.sl.cumsum(0).to(torch.int32)]),
+                                  int(self.sl.sum()), k_block_scales=self.ks)
+            self.qkv = torch.zeros(S, (Hq + 2 * Hkv) * D, dtype=torch.bfloat16, device="cuda")
+            self.pos = torch.zeros(S, dtype=torch.int64, device="cuda")
+            self.qo = torch.empty(S, Hq, D, dtype=torch.bfloat16, device="cuda")
+            self.ko = torch.empty(S, Hkv, D, dtype=torch.bfloat16, device="cuda")
+            self.sel = torch.empty(S, Hkv, keep, dtype=torch.int32, device="cuda")
+            self.out = torch.empty_like(self.qo)
+
+        def step(self):
+            q, k, v = (x.unflatten(1, (-1, D)) for x in self.qkv.split([Hq * D, Hkv * D, Hkv * D], 1))
+            pkv.qk_norm_rope(self.qo, self.ko, q, k, w, w, 1e-6, cs, self.pos)
+            pkv.reshape_and_cache_block_scales(self.ko, v, self.kc, self.vc, self.ks, self.vs, dt, self.sl, ro)
+            pkv.update_key_bounds(self.kb, self.kc, dt, self.sl, ro, S, k_block_scales=self.ks)
+            pkv.select_blocks(self.sel, self.qo, self.kb, dt, self.sl, block)
+            pkv.paged_attention_decode_sparse(self.out, self.qo, self.kc, self.vc, dt, self.sl, self.sel, 0.1,
+                                              k_block_scales=self.ks, v_block_scales=self.vs)
+
+        def feed(self, i):
+            g = torch.Generator(device="cuda").manual_seed(100 + i)
+            self.qkv.copy_(torch.randn(self.qkv.shape, generator=g, device="cuda"))
+            self.sl += 1
+            self.pos.copy_(self.sl.long() - 1)
+
+    eager, other = Run(), Run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        other.step()
+    for i in range(6):
+        eager.feed(i)
+        eager.step()
+        other.feed(i)
+        graph.replay()
+        for x in ("qo", "sel", "out", "ks", "vs", "kb"):
+            assert torch.equal(getattr(eager, x), getattr(other, x)), x
+        assert torch.equal(eager.kc.view(torch.uint8), other.kc.view(torch.uint8))

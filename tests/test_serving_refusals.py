@@ -273,3 +273,31 @@ def test_select_bindings(fake):
         with pytest.raises((TypeError, ValueError)):
             pkv.select_blocks(**{**x, **bad})
     assert not fake.calls
+
+
+def test_tensors_on_another_device_are_refused(fake):
+    far = lambda *shape, dtype=torch.bfloat16: cuda(torch.zeros(*shape, dtype=dtype), 1)
+    x = rope_inputs()
+    for name, bad in (("q", far(3, 8, 64)), ("v", far(3, 2, 64)), ("cos_sin", far(10, 32, dtype=torch.float32)),
+                      ("v_cache", far(4, 2, 16, 64)), ("q_out", far(3, 8, 64))):
+        with pytest.raises(ValueError):
+            pkv.qk_norm_rope_and_cache(**{**x, name: bad})
+    sel = dict(selected=i32(3, 2, 5), q=bf(3, 8, 128), key_bounds=bf(4, 2, 2, 128), block_tables=i32(3, 6), seq_lens=i32(3),
+               block_size=16, workspace=u8(1 << 16))
+    for name, bad in (("key_bounds", far(4, 2, 2, 128)), ("workspace", far(1 << 16, dtype=torch.uint8)),
+                      ("selected", far(3, 2, 5, dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            pkv.select_blocks(**{**sel, name: bad})
+    assert not fake.calls
+
+
+def test_views_that_are_not_contiguous_are_refused(fake):
+    x = rope_inputs()
+    with pytest.raises(ValueError):
+        pkv.qk_norm_rope_and_cache(**{**x, "q_out": cuda(torch.zeros(3, 8, 128, dtype=torch.bfloat16)[:, :, ::2])})
+    with pytest.raises(ValueError):
+        pkv.qk_norm_rope_and_cache(**{**x, "k_cache": cuda(torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16).transpose(1, 2))})
+    with pytest.raises(ValueError):
+        pkv.update_key_bounds(bf(4, 2, 2, 128), bf(4, 2, 16, 128), cuda(torch.zeros(3, 12, dtype=torch.int32)[:, ::2]),
+                              i32(3), i32(4), 9)
+    assert not fake.calls
