@@ -121,8 +121,52 @@ def load_library():
     lib.pkv_validate_tables.restype = i32
     lib.pkv_status_string.argtypes = [i32]
     lib.pkv_status_string.restype = ctypes.c_char_p
+    _bind_fast(lib)
     _lib = lib
     return lib
+
+
+# The hot path of the operators that a serving loop calls once per layer (csrc/fastcall.cpp), where it
+# is built: their C functions without ctypes' conversions, and the checks of a call's tensors in one
+# go. What the module does not pass, the checks below look at one by one and explain.
+_fast = None
+_SPECS: dict = {}
+
+
+def _bind_fast(lib) -> None:
+    global _fast
+    try:
+        from . import _fastcall
+    except ImportError:
+        return
+    for name in ("qk_norm_rope", "qk_norm_rope_and_cache", "reshape_and_cache_block_scales",
+                 "paged_attention_decode_block_scales", "update_key_bounds", "select_blocks",
+                 "paged_attention_decode_sparse"):
+        _fastcall.bind(name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value)
+        setattr(lib, name, getattr(_fastcall, name))
+    caches = "k_cache:N,Hkv,B,D:c:K v_cache:N,Hkv,B,D:c:K"
+    tables = "block_tables:S,M:c:i seq_lens:S:c:i"
+    norm = ("q:T,Hq,D:rows:X k:T,Hkv,D:rows:X q_out:T,Hq,D:c:X q_weight:D:c:X k_weight:D:c:X cos_sin:P,R:c:f "
+            "positions:T:c:l")
+    decode = f"q:S,Hq,D:c:X out:S,Hq,D:c:X {caches} {tables}"
+    _SPECS.update({name: _fastcall.spec(text) for name, text in {
+        "norm": f"{norm} k_out:T,Hkv,D:c:X",
+        "norm_cache": f"{norm} v:T,Hkv,D:rows:X {caches} slot_mapping:T:c:l",
+        "append": f"k:T,Hkv,D:rows:X v:T,Hkv,D:rows:X {caches} k_scales:N,Hkv:c:f v_scales:N,Hkv:c:f {tables} "
+                  "row_offsets:S+1:c:i",
+        "decode": f"{decode} k_scales:N,Hkv:c:f v_scales:N,Hkv:c:f",
+        "sparse": f"{decode} selected:S,Hkv,W:c:i ?k_scales:N,Hkv:c:f ?v_scales:N,Hkv:c:f",
+        "bounds": f"key_bounds:N,Hkv,2,D:c:b k_cache:N,Hkv,B,D:c:K {tables} row_offsets:S+1:c:i ?k_scales:N,Hkv:c:f",
+        "select": f"selected:S,Hkv,W:c:i q:S,Hq,D:c:b key_bounds:N,Hkv,2,D:c:b {tables}",
+    }.items()})
+    _fast = _fastcall
+
+
+def _match(name, *tensors):
+    """The pieces of a call's tensors (pointers, sizes in the spec's order, row strides, type codes, the
+    device) if every check passes, else None."""
+    load_library()
+    return None if _fast is None else _fast.match(_SPECS[name], *tensors)
 
 
 def status_string(status: int) -> str:
@@ -566,13 +610,18 @@ def qk_norm_rope(q_out, k_out, q, k, q_weight, k_weight, eps, cos_sin, positions
     views of a larger projection output are fine); q_out, k_out contiguous, or q and k themselves;
     weights [head_dim]; cos_sin float32 [num_positions, rotary_dim] (cosines, then sines);
     positions int64 [num_tokens]."""
-    dev = _launch_device("q", q)
-    qp, kp, T, Hq, Hkv, D, qs, ks, qo, qw, kw, cs, pos, NP, R, dt = _norm_rope_args(
-        q_out, q, k, q_weight, k_weight, cos_sin, positions, dev)
-    if k_out.shape != (T, Hkv, D) or k_out.dtype != q.dtype:
-        raise ValueError("k_out must match k")
+    m = _match("norm", q, k, q_out, q_weight, k_weight, cos_sin, positions, k_out)
+    if m is not None:
+        qp, kp, qo, qw, kw, cs, pos, ko, T, Hq, D, Hkv, NP, R, qs, ks, dt, dev = m
+    else:
+        dev = _launch_device("q", q)
+        qp, kp, T, Hq, Hkv, D, qs, ks, qo, qw, kw, cs, pos, NP, R, dt = _norm_rope_args(
+            q_out, q, k, q_weight, k_weight, cos_sin, positions, dev)
+        if k_out.shape != (T, Hkv, D) or k_out.dtype != q.dtype:
+            raise ValueError("k_out must match k")
+        ko = _ptr("k_out", k_out, dev)
     _check("qk_norm_rope", load_library().qk_norm_rope(
-        qo, _ptr("k_out", k_out, dev), qp, kp, qw, kw, float(eps), cs, pos, T, Hq, Hkv, D, R, NP, bool(interleaved), qs, ks, dt,
+        qo, ko, qp, kp, qw, kw, float(eps), cs, pos, T, Hq, Hkv, D, R, NP, bool(interleaved), qs, ks, dt,
         _opt_ptr("device_error", device_error, dev), _raw_stream(stream, dev)))
 
 
@@ -581,22 +630,28 @@ def qk_norm_rope_and_cache(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, pos
                            stream=None) -> None:
     """qk_norm_rope with the append of reshape_and_cache in the same pass: the new keys and the rows
     of v go to slot slot_mapping[t] of the caches (a negative slot appends nothing)."""
-    dev = _launch_device("q", q)
-    qp, kp, T, Hq, Hkv, D, qs, ks, qo, qw, kw, cs, pos, NP, R, dt = _norm_rope_args(
-        q_out, q, k, q_weight, k_weight, cos_sin, positions, dev)
-    vp, Tv, _, _, vs = _rows("v", v, dev, heads=Hkv, dim=D, dtype=q.dtype)
-    shape = k_cache.shape
-    NB, Hkv2, BS, D2 = shape
-    if Tv != T or Hkv2 != Hkv or D2 != D or v_cache.shape != shape:
-        raise ValueError("shape mismatch between rows and caches")
-    if v_cache.dtype != k_cache.dtype:
-        raise TypeError("v_cache must have k_cache's dtype")
-    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
-        raise TypeError("slot_mapping must be int64 [num_tokens]")
+    m = _match("norm_cache", q, k, q_out, q_weight, k_weight, cos_sin, positions, v, k_cache, v_cache, slot_mapping)
+    if m is not None:
+        (qp, kp, qo, qw, kw, cs, pos, vp, kc, vc, sm, T, Hq, D, Hkv, NP, R, NB, BS, qs, ks, vs, dt, kdt, dev) = m
+    else:
+        dev = _launch_device("q", q)
+        qp, kp, T, Hq, Hkv, D, qs, ks, qo, qw, kw, cs, pos, NP, R, dt = _norm_rope_args(
+            q_out, q, k, q_weight, k_weight, cos_sin, positions, dev)
+        vp, Tv, _, _, vs = _rows("v", v, dev, heads=Hkv, dim=D, dtype=q.dtype)
+        shape = k_cache.shape
+        NB, Hkv2, BS, D2 = shape
+        if Tv != T or Hkv2 != Hkv or D2 != D or v_cache.shape != shape:
+            raise ValueError("shape mismatch between rows and caches")
+        if v_cache.dtype != k_cache.dtype:
+            raise TypeError("v_cache must have k_cache's dtype")
+        if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
+            raise TypeError("slot_mapping must be int64 [num_tokens]")
+        kc, vc, kdt = _ptr("k_cache", k_cache, dev), _ptr("v_cache", v_cache, dev), _dtype_code(k_cache)
+        sm = _ptr("slot_mapping", slot_mapping, dev)
     _check("qk_norm_rope_and_cache", load_library().qk_norm_rope_and_cache(
-        qo, qp, kp, vp, qw, kw, float(eps), cs, pos, _ptr("k_cache", k_cache, dev), _ptr("v_cache", v_cache, dev),
-        _ptr("slot_mapping", slot_mapping, dev), T, Hq, Hkv, D, R, NP, BS, NB, bool(interleaved), qs, ks, vs, dt,
-        _dtype_code(k_cache), float(k_scale), float(v_scale), _opt_ptr("device_error", device_error, dev), _raw_stream(stream, dev)))
+        qo, qp, kp, vp, qw, kw, float(eps), cs, pos, kc, vc, sm, T, Hq, Hkv, D, R, NP, BS, NB, bool(interleaved), qs,
+        ks, vs, dt, kdt, float(k_scale), float(v_scale), _opt_ptr("device_error", device_error, dev),
+        _raw_stream(stream, dev)))
 
 
 def _tables(block_tables, seq_lens, dev):
@@ -629,22 +684,28 @@ def reshape_and_cache_block_scales(k, v, k_cache, v_cache, k_block_scales, v_blo
     newest tokens of sequence s, which has seq_lens[s] tokens with them. The scales (float32
     [num_blocks, num_kv_heads]) of the blocks they fall into are set, or grow (and the block's older
     codes with them) where the block already holds tokens of the sequence."""
-    dev = _launch_device("k", k)
-    kp, T, Hkv, D, ks = _rows("k", k, dev)
-    vp, Tv, _, _, vs = _rows("v", v, dev, heads=Hkv, dim=D, dtype=k.dtype)
-    shape = k_cache.shape
-    NB, Hkv2, BS, D2 = shape
-    if Tv != T or Hkv2 != Hkv or D2 != D or v_cache.shape != shape:
-        raise ValueError("shape mismatch between rows and caches")
-    if v_cache.dtype != k_cache.dtype:
-        raise TypeError("v_cache must have k_cache's dtype")
-    bt, sl, S, MB = _tables(block_tables, seq_lens, dev)
+    m = _match("append", k, v, k_cache, v_cache, k_block_scales, v_block_scales, block_tables, seq_lens, row_offsets)
+    if m is not None:
+        kp, vp, kc, vc, kbs, vbs, bt, sl, ro, T, Hkv, D, NB, BS, S, MB, ks, vs, dt, kdt, dev = m
+    else:
+        dev = _launch_device("k", k)
+        kp, T, Hkv, D, ks = _rows("k", k, dev)
+        vp, Tv, _, _, vs = _rows("v", v, dev, heads=Hkv, dim=D, dtype=k.dtype)
+        shape = k_cache.shape
+        NB, Hkv2, BS, D2 = shape
+        if Tv != T or Hkv2 != Hkv or D2 != D or v_cache.shape != shape:
+            raise ValueError("shape mismatch between rows and caches")
+        if v_cache.dtype != k_cache.dtype:
+            raise TypeError("v_cache must have k_cache's dtype")
+        bt, sl, S, MB = _tables(block_tables, seq_lens, dev)
+        ro = _row_offsets(row_offsets, S, dev)
+        kbs = _block_scales("k_block_scales", k_block_scales, shape, dev)
+        vbs = _block_scales("v_block_scales", v_block_scales, shape, dev)
+        kc, vc = _ptr("k_cache", k_cache, dev), _ptr("v_cache", v_cache, dev)
+        dt, kdt = _dtype_code(k), _dtype_code(k_cache)
     _check("reshape_and_cache_block_scales", load_library().reshape_and_cache_block_scales(
-        kp, vp, _ptr("k_cache", k_cache, dev), _ptr("v_cache", v_cache, dev),
-        _block_scales("k_block_scales", k_block_scales, shape, dev),
-        _block_scales("v_block_scales", v_block_scales, shape, dev), bt, sl, _row_offsets(row_offsets, S, dev), T, S,
-        Hkv, D, BS, MB, NB, ks, vs, _dtype_code(k), _dtype_code(k_cache), _opt_ptr("device_error", device_error, dev),
-        _raw_stream(stream, dev)))
+        kp, vp, kc, vc, kbs, vbs, bt, sl, ro, T, S, Hkv, D, BS, MB, NB, ks, vs, dt, kdt,
+        _opt_ptr("device_error", device_error, dev), _raw_stream(stream, dev)))
 
 
 def _decode_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, dev):
@@ -667,17 +728,23 @@ def paged_attention_decode_block_scales(out, q, k_cache, v_cache, block_tables, 
                                         v_block_scales, num_partitions=0, workspace=None, stream=None) -> None:
     """paged_attention_decode over an 8-bit cache with one scale for each (block, KV head):
     k_block_scales, v_block_scales float32 [num_blocks, num_kv_heads], positive."""
-    dev = _launch_device("q", q)
-    S, Hq, D, cache, op, qp, kp, vp, bt, sl, MB = _decode_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, dev)
-    NB, Hkv, BS, _ = cache
-    ks = _block_scales("k_block_scales", k_block_scales, cache, dev)
-    vs = _block_scales("v_block_scales", v_block_scales, cache, dev)
+    m = _match("decode", q, out, k_cache, v_cache, block_tables, seq_lens, k_block_scales, v_block_scales)
+    if m is not None:
+        qp, op, kp, vp, bt, sl, ks, vs, S, Hq, D, NB, Hkv, BS, MB, dt, kdt, dev = m
+    else:
+        dev = _launch_device("q", q)
+        S, Hq, D, cache, op, qp, kp, vp, bt, sl, MB = _decode_shapes(out, q, k_cache, v_cache, block_tables, seq_lens,
+                                                                     dev)
+        NB, Hkv, BS, _ = cache
+        ks = _block_scales("k_block_scales", k_block_scales, cache, dev)
+        vs = _block_scales("v_block_scales", v_block_scales, cache, dev)
+        dt, kdt = _dtype_code(q), _dtype_code(k_cache)
     st = _raw_stream(stream, dev)
     if workspace is None:
         workspace = _op_workspace("decode", _sized(workspace_size, dev, S, Hq, Hkv, D, num_partitions), dev, st)
     _check("paged_attention_decode_block_scales", load_library().paged_attention_decode_block_scales(
-        op, qp, kp, vp, bt, sl, S, Hq, Hkv, D, BS, float(scale), MB, NB, _dtype_code(q), _dtype_code(k_cache), ks, vs,
-        int(num_partitions), _ptr("workspace", workspace, dev), workspace.numel(), st))
+        op, qp, kp, vp, bt, sl, S, Hq, Hkv, D, BS, float(scale), MB, NB, dt, kdt, ks, vs, int(num_partitions),
+        _ptr("workspace", workspace, dev), workspace.numel(), st))
 
 
 def update_key_bounds(key_bounds, k_cache, block_tables, seq_lens, row_offsets, num_tokens, k_scale=1.0,
@@ -685,16 +752,21 @@ def update_key_bounds(key_bounds, k_cache, block_tables, seq_lens, row_offsets, 
     """Refresh key_bounds (bfloat16 [num_blocks, num_kv_heads, 2, head_dim]: maxima, minima over a
     block's keys) for the blocks that hold the num_tokens newest tokens of a batch, after their
     append; row_offsets as in reshape_and_cache_block_scales (int32 [num_seqs + 1])."""
-    dev = _launch_device("k_cache", k_cache)
-    shape = k_cache.shape
-    NB, Hkv, BS, D = shape
-    if key_bounds.dtype != torch.bfloat16 or key_bounds.shape != (NB, Hkv, 2, D):
-        raise TypeError("key_bounds must be bfloat16 [num_blocks, num_kv_heads, 2, head_dim]")
-    bt, sl, S, MB = _tables(block_tables, seq_lens, dev)
-    scales = None if k_block_scales is None else _block_scales("k_block_scales", k_block_scales, shape, dev)
+    m = _match("bounds", key_bounds, k_cache, block_tables, seq_lens, row_offsets, k_block_scales)
+    if m is not None:
+        kb, kc, bt, sl, ro, scales, NB, Hkv, D, BS, S, MB, kdt, dev = m
+    else:
+        dev = _launch_device("k_cache", k_cache)
+        shape = k_cache.shape
+        NB, Hkv, BS, D = shape
+        if key_bounds.dtype != torch.bfloat16 or key_bounds.shape != (NB, Hkv, 2, D):
+            raise TypeError("key_bounds must be bfloat16 [num_blocks, num_kv_heads, 2, head_dim]")
+        bt, sl, S, MB = _tables(block_tables, seq_lens, dev)
+        ro = _row_offsets(row_offsets, S, dev)
+        scales = None if k_block_scales is None else _block_scales("k_block_scales", k_block_scales, shape, dev)
+        kb, kc, kdt = _ptr("key_bounds", key_bounds, dev), _ptr("k_cache", k_cache, dev), _dtype_code(k_cache)
     _check("update_key_bounds", load_library().update_key_bounds(
-        _ptr("key_bounds", key_bounds, dev), _ptr("k_cache", k_cache, dev), bt, sl, _row_offsets(row_offsets, S, dev),
-        int(num_tokens), S, Hkv, D, BS, MB, NB, _dtype_code(k_cache), float(k_scale), scales,
+        kb, kc, bt, sl, ro, int(num_tokens), S, Hkv, D, BS, MB, NB, kdt, float(k_scale), scales or None,
         _opt_ptr("device_error", device_error, dev), _raw_stream(stream, dev)))
 
 
@@ -718,24 +790,28 @@ def select_blocks(selected, q, key_bounds, block_tables, seq_lens, block_size, n
     num_sink_blocks, the last num_recent_blocks and the highest scores of the rest, a block's score
     being the bound that key_bounds sets to its keys' products with the group's queries.
     q bfloat16 [num_seqs, num_heads, head_dim]."""
-    dev = _launch_device("q", q)
-    S, Hq, D = q.shape
-    NB, Hkv, two, D2 = key_bounds.shape
-    if q.dtype != torch.bfloat16 or key_bounds.dtype != torch.bfloat16:
-        raise TypeError("q and key_bounds must be bfloat16")
-    if two != 2 or D2 != D:
-        raise ValueError("key_bounds must be [num_blocks, num_kv_heads, 2, head_dim]")
-    W = _selected_width(selected, S, Hkv)
-    bt, sl, S2, MB = _tables(block_tables, seq_lens, dev)
-    if S2 != S:
-        raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
+    m = _match("select", selected, q, key_bounds, block_tables, seq_lens)
+    if m is not None:
+        sel, qp, kb, bt, sl, S, Hkv, W, Hq, D, NB, MB, dev = m
+    else:
+        dev = _launch_device("q", q)
+        S, Hq, D = q.shape
+        NB, Hkv, two, D2 = key_bounds.shape
+        if q.dtype != torch.bfloat16 or key_bounds.dtype != torch.bfloat16:
+            raise TypeError("q and key_bounds must be bfloat16")
+        if two != 2 or D2 != D:
+            raise ValueError("key_bounds must be [num_blocks, num_kv_heads, 2, head_dim]")
+        W = _selected_width(selected, S, Hkv)
+        bt, sl, S2, MB = _tables(block_tables, seq_lens, dev)
+        if S2 != S:
+            raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
+        sel, qp, kb = _ptr("selected", selected, dev), _ptr("q", q, dev), _ptr("key_bounds", key_bounds, dev)
     st = _raw_stream(stream, dev)
     if workspace is None:
         workspace = _op_workspace("select", _sized(select_workspace_size, dev, S, Hkv, max(1, MB)), dev, st)
     _check("select_blocks", load_library().select_blocks(
-        _ptr("selected", selected, dev), _ptr("q", q, dev), _ptr("key_bounds", key_bounds, dev), bt, sl, S, Hq, Hkv, D,
-        int(block_size), MB, NB, W, int(num_sink_blocks), int(num_recent_blocks), _ptr("workspace", workspace, dev),
-        workspace.numel(), st))
+        sel, qp, kb, bt, sl, S, Hq, Hkv, D, int(block_size), MB, NB, W, int(num_sink_blocks), int(num_recent_blocks),
+        _ptr("workspace", workspace, dev), workspace.numel(), st))
 
 
 def _selected_width(selected, S, Hkv) -> int:
@@ -751,22 +827,28 @@ def paged_attention_decode_sparse(out, q, k_cache, v_cache, block_tables, seq_le
     """paged_attention_decode over the tokens of the listed blocks only: selected int32 [num_seqs,
     num_kv_heads, num_selected] (select_blocks' output), negative entries empty. 8-bit caches take
     per-tensor scales or both block scales."""
-    dev = _launch_device("q", q)
-    S, Hq, D, cache, op, qp, kp, vp, bt, sl, MB = _decode_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, dev)
-    NB, Hkv, BS, _ = cache
-    W = _selected_width(selected, S, Hkv)
     if (k_block_scales is None) != (v_block_scales is None):
         raise ValueError("give both block scales or none")
-    ks = vs = None
-    if k_block_scales is not None:
-        ks = _block_scales("k_block_scales", k_block_scales, cache, dev)
-        vs = _block_scales("v_block_scales", v_block_scales, cache, dev)
+    m = _match("sparse", q, out, k_cache, v_cache, block_tables, seq_lens, selected, k_block_scales, v_block_scales)
+    if m is not None:
+        qp, op, kp, vp, bt, sl, sel, ks, vs, S, Hq, D, NB, Hkv, BS, MB, W, dt, kdt, dev = m
+    else:
+        dev = _launch_device("q", q)
+        S, Hq, D, cache, op, qp, kp, vp, bt, sl, MB = _decode_shapes(out, q, k_cache, v_cache, block_tables, seq_lens,
+                                                                     dev)
+        NB, Hkv, BS, _ = cache
+        W = _selected_width(selected, S, Hkv)
+        ks = vs = None
+        if k_block_scales is not None:
+            ks = _block_scales("k_block_scales", k_block_scales, cache, dev)
+            vs = _block_scales("v_block_scales", v_block_scales, cache, dev)
+        sel, dt, kdt = _ptr("selected", selected, dev), _dtype_code(q), _dtype_code(k_cache)
     st = _raw_stream(stream, dev)
     if workspace is None:
         workspace = _op_workspace("decode", _sized(workspace_size, dev, S, Hq, Hkv, D, num_partitions), dev, st)
     _check("paged_attention_decode_sparse", load_library().paged_attention_decode_sparse(
-        op, qp, kp, vp, bt, sl, _ptr("selected", selected, dev), S, Hq, Hkv, D, BS, float(scale), MB, NB, W,
-        _dtype_code(q), _dtype_code(k_cache), float(k_scale), float(v_scale), ks, vs, int(num_partitions), _ptr("workspace", workspace, dev),
+        op, qp, kp, vp, bt, sl, sel, S, Hq, Hkv, D, BS, float(scale), MB, NB, W, dt, kdt, float(k_scale),
+        float(v_scale), ks or None, vs or None, int(num_partitions), _ptr("workspace", workspace, dev),
         workspace.numel(), st))
 
 

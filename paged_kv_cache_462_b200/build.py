@@ -3,21 +3,25 @@
     python -m paged_kv_cache_462_b200.build [--force]
 
 Each .cu file compiles to an object in parallel; the objects link into
-``paged_kv_cache_462_b200/libpagedkv.so`` (the CUDA runtime linked statically).
+``paged_kv_cache_462_b200/libpagedkv.so`` (the CUDA runtime linked statically). The binding's
+hot path, ``csrc/fastcall.cpp``, becomes the extension module ``_fastcall.so`` beside it.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libpagedkv.so")
+FASTCALL = os.path.join(HERE, "_fastcall.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -41,14 +45,37 @@ def _deps():
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _newer(target, deps) -> bool:
+    if not os.path.exists(target):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(f) <= t for f in deps)
+
+
+def up_to_date() -> bool:
+    return _newer(LIB, _deps())
+
+
+def build_fastcall(force: bool = False) -> str:
+    """The extension module _fastcall.so (g++, torch's and Python's headers)."""
+    src = os.path.join(CSRC, "fastcall.cpp")
+    if not force and _newer(FASTCALL, [src, os.path.join(INCLUDE, "pkv.h")]):
+        return FASTCALL
+    torch_dir = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    tmp = FASTCALL + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"),
+           "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), src,
+           "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, FASTCALL)
+    return FASTCALL
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_fastcall(force)
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)

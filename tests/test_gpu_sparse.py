@@ -518,3 +518,45 @@ def test_a_step_captured_and_replayed():
         for x in ("qo", "sel", "out", "ks", "vs", "kb"):
             assert torch.equal(getattr(eager, x), getattr(other, x)), x
         assert torch.equal(eager.kc.view(torch.uint8), other.kc.view(torch.uint8))
+
+
+def test_the_binding_without_its_hot_path(monkeypatch):
+    """The same calls through ctypes and the step-by-step checks, as where _fastcall is not built."""
+    gen = torch.Generator().manual_seed(51)
+    lens, new = [300, 17, 64], [300, 17, 64]
+    table, pool = plain.tables(lens, 16, gen)
+    dt, sl = table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    ro = torch.tensor([0, 300, 317, 381], dtype=torch.int32).cuda()
+    qkv = torch.randn(381, 12 * 128, generator=gen).to(torch.bfloat16).cuda()
+    q, k, v = (x.unflatten(1, (-1, 128)) for x in qkv.split([1024, 256, 256], 1))
+    w = torch.ones(128, dtype=torch.bfloat16, device="cuda")
+    cs, pos = torch.randn(400, 128, generator=gen).cuda(), torch.arange(381, device="cuda")
+
+    def run():
+        kc = torch.zeros(pool, 2, 16, 128, dtype=torch.int8, device="cuda")
+        vc, ks, vs = torch.zeros_like(kc), torch.zeros(pool, 2, device="cuda"), torch.zeros(pool, 2, device="cuda")
+        kb = torch.zeros(pool, 2, 2, 128, dtype=torch.bfloat16, device="cuda")
+        k16, v16 = (torch.zeros(pool + 9, 2, 16, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        qo, ko = torch.empty(381, 8, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(381, 2, 128, dtype=torch.bfloat16, device="cuda")
+        pkv.qk_norm_rope(qo, ko, q, k, w, w, 1e-6, cs, pos)
+        pkv.qk_norm_rope_and_cache(torch.empty_like(qo), q, k, v, w, w, 1e-6, cs, pos, k16, v16, pos)
+        pkv.reshape_and_cache_block_scales(ko, v, kc, vc, ks, vs, dt, sl, ro)
+        pkv.update_key_bounds(kb, kc, dt, sl, ro, 381, k_block_scales=ks)
+        qq = qo[[299, 316, 380]].contiguous()
+        sel = torch.empty(3, 2, 5, dtype=torch.int32, device="cuda")
+        o1, o2, o3 = torch.empty_like(qq), torch.empty_like(qq), torch.empty_like(qq)
+        pkv.select_blocks(sel, qq, kb, dt, sl, 16)
+        pkv.paged_attention_decode_block_scales(o1, qq, kc, vc, dt, sl, 0.1, ks, vs)
+        pkv.paged_attention_decode_sparse(o2, qq, kc, vc, dt, sl, sel, 0.1, k_block_scales=ks, v_block_scales=vs)
+        pkv.paged_attention_decode_sparse(o3, qq, kc, vc, dt, sl, sel, 0.1, 0.02, 0.02)
+        return kc, vc, ks, vs, kb, qo, ko, k16, v16, sel, o1, o2, o3
+
+    pkv.load_library()
+    assert pkv._fast is not None, "csrc/fastcall.cpp is not built"
+    want = run()
+    monkeypatch.setattr(pkv, "_fast", None)
+    monkeypatch.setattr(pkv, "_lib", None)
+    monkeypatch.setattr(pkv, "_bind_fast", lambda lib: None)
+    got = run()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
