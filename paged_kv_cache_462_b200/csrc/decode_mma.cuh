@@ -276,7 +276,11 @@ __device__ __forceinline__ size_t query_row(const DecodeParams& p, int s, int he
 // group (HG = 1) and the kNT = 4 consumer warps take its 32 query columns (the group's members x
 // their query heads), 8 each, against the same staged K/V tile.
 // PH: every KV head of a unit is resolved for itself by the producer (UnitHead): its block of a
-// sparse decode, its scales of a cache with block scales.
+// sparse decode (then a box of block_size rows per head and 128 bytes; all heads in one otherwise), its
+// scales of a cache with block scales. Bound as the kernel without it: 64 sequences x 128 selected
+// blocks, bf16 (536 MB) 96.5 us, 5.6 TB/s, 85 % of the copy rate; 128 x 1024-1280 tokens, E4M3 with
+// block scales (305 MB) 68.5 us, 68 % (per-tensor scales 70 us), and 16 x 24001-32768, INT8 (938 MB) 168
+// us, 85 %, both by the consumer warps' latency (12 an SM, 43-47 % of the issue slots).
 template <class KV, int D, int BS, int G, int HG, bool PFX = false, bool PH = false>
 struct MmaCfg {
     // products: bf16 caches in bf16 MMA; 8-bit codes widened exactly to f16 (widen_halves) for f16 MMA,

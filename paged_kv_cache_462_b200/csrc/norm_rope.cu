@@ -6,8 +6,10 @@
 //                                               the token's row of the cos / sin table
 //
 // Everything is fp32 from the load to the one rounding of each stored element; the sum of
-// squares is fp32 too. Bound: HBM (each row is read once and written once, about 8 operations an
-// element).
+// squares is fp32 too. Bound: HBM (each row is read once and written once), with the issue slots not
+// far behind. Measured (40 query and 8 KV heads of 128, bf16, 8192 tokens, 239 MB): 44.8 us, 5.3 TB/s,
+// 82 % of the copy rate; with a CTA per token and a load per row 63 us, 70 % of the issue slots busy.
+// Four tokens: 3.5 us, launch and latency.
 //
 // Layout: a row is held by head_dim / 8 lanes (16 or 8), 8 elements each, as two chunks of four
 // chosen so that both elements of a rotation pair lie in one lane: chunks (4c, rotary/2 + 4c) for
@@ -166,7 +168,8 @@ struct NormSmem {
 };
 
 // WHOLE: half-split pairs over the whole head (rotary == D), what most models use: the chunks' places
-// are known when this is compiled. CACHED: K and V go to the caches.
+// are known when this is compiled (8192 tokens as above: 44.8 us, the general form 58.7 us; four
+// tokens 3.5 and 4.0 us). CACHED: K and V go to the caches.
 template <class TIN, class TC, int D, __nv_fp8_interpretation_t FMT, bool WHOLE, bool CACHED>
 __global__ void __launch_bounds__(kNormThreads + 32, sizeof(TIN) == 2 ? 3 : 2) norm_rope_kernel(const NormRopeArgs p)
 {

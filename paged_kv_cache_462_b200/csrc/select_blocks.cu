@@ -28,6 +28,13 @@
 // queued behind it as a dependent launch, selects, a CTA per stream: up to 2048 blocks (or 16384, with
 // four times the threads) are kept in registers, with as few exchanges as the steps allow: latency is
 // all it costs.
+//
+// Measured (32 query and 8 KV heads of 128, blocks of 16): 64 sequences of 20001 to 32768 tokens, 128 of
+// up to 2048 blocks (434 MB) 84.6 us, of which the scores take 74 (5.9 TB/s, 89 % of the copy rate) and
+// the selection 11; 16 x 8192 tokens (34 MB) 14.5 us, 8 of them the latency of the two launches' chains
+// of loads. One launch, its last CTA of a stream selecting, took 100 us: a CTA that selects streams
+// nothing. A warp per stream selected 2048 blocks in 53 us, a CTA in shared memory in 20, in registers
+// in 11; one sequence of 131072 tokens (8192 blocks) 50 us in shared memory, 21 us with 1024 threads.
 #include <cstdint>
 
 #include "device.cuh"
