@@ -546,6 +546,7 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
         bool aborted = false;
         int issued = 0;
         int k = 0;                 // stages issued so far (ring position)
+        [[maybe_unused]] int st = 0, lap = 0;   // k % stages, k / stages (PH)
         int published = 0;         // chunks announced to the consumers
         while (cur < ch.C && !aborted) {
             const int cb = ch.begin(cur);
@@ -650,8 +651,7 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
                         ahead = resolve(k0 + 32 + lane);
                     }
                     const int cnt = min(32, nunits - k0);
-                    for (int i = 0; i < cnt && !aborted; ++i, ++k) {
-                        const int st = k % S;
+                    for (int i = 0; i < cnt && !aborted; ++i) {
                         // lane w takes head w's entry
                         int row = -1, valid = 0;
                         float ks = 1.f, vs = 1.f;
@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
                         if (lane == 0) {
                             if (*abort_flag) {
                                 aborted = true;
-                            } else if (k >= S && !mbar_wait_bounded(&empty[st], ((k / S) - 1) & 1)) {
+                            } else if (lap > 0 && !mbar_wait_bounded(&empty[st], (lap - 1) & 1)) {
                                 aborted = true;
                                 *abort_flag = 1;
                                 atomicOr(p.err, PKV_DEVERR_TIMEOUT);
@@ -715,6 +715,11 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
                                 tma_load_2d(at, &kmap, bx * C::kBoxCols, row, &full[st]);
                                 tma_load_2d(at + C::kHalf, &vmap, bx * C::kBoxCols, row, &full[st]);
                             }
+                        }
+                        ++k;
+                        if (++st == S) {
+                            st = 0;
+                            ++lap;
                         }
                     }
                 }
@@ -798,12 +803,12 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
     const int t = lane & 3;    // MMA column pair
 
 
-    int k = 0;                 // stages consumed so far (ring position)
+    int st = 0;                // ring position: the stage, and the parity of its turn
+    uint32_t turn = 0;
     for (int ordinal = 0;; ++ordinal) {
         // the first stage of the CTA's next chunk carries the chunk's id (-1: no more work)
         {
-            const int st = k % S;
-            const bool ok = !*abort_flag && mbar_wait_bounded(&full[st], (k / S) & 1);
+            const bool ok = !*abort_flag && mbar_wait_bounded(&full[st], turn);
             if (!__all_sync(kFullMask, ok)) {
                 if (lane == 0 && !*abort_flag) {
                     *abort_flag = 1;
@@ -947,9 +952,8 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
             float m[2] = {-INFINITY, -INFINITY};   // running reference for heads 2t, 2t+1
             float l[2] = {0.f, 0.f};
 
-            for (; x < seg_end; ++x, ++k) {
-                const int st = k % S;
-                bool ok = !*abort_flag && mbar_wait_bounded(&full[st], (k / S) & 1);
+            for (; x < seg_end; ++x) {
+                bool ok = !*abort_flag && mbar_wait_bounded(&full[st], turn);
                 if (__any_sync(kFullMask, !ok)) {
                     if (lane == 0 && !*abort_flag) {
                         *abort_flag = 1;
@@ -965,7 +969,7 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
                     valid = uh.valid;
                 }
                 bool released = false;
-                if (ok && skip[st] == 0 && valid > 0) {
+                if (ok && (PH || skip[st] == 0) && valid > 0) {
                     const uint32_t kbase = smem_addr(stages + (size_t)st * C::kStage);
                     const uint32_t vbase = kbase + C::kHalf;
                     const int r0 = (warp / C::kNT) * BS;   // this warp's KV head's first box row
@@ -1064,10 +1068,16 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
                             const int n0 = 2 * t < G ? valid : 0, n1 = 2 * t + 1 < G ? valid : 0;
                             const float f0 = F16 ? qk0 * uh.ks : qk0, f1 = F16 ? qk1 * uh.ks : qk1;
                             const float add = F16 ? uh.log2_vs : 0.f;
-                            sc[0] = (row0_ < n0) ? fmaf(sc[0], f0, add) : -INFINITY;
-                            sc[1] = (row0_ < n1) ? fmaf(sc[1], f1, add) : -INFINITY;
-                            sc[2] = (row8_ < n0) ? fmaf(sc[2], f0, add) : -INFINITY;
-                            sc[3] = (row8_ < n1) ? fmaf(sc[3], f1, add) : -INFINITY;
+                            sc[0] = fmaf(sc[0], f0, add);
+                            sc[1] = fmaf(sc[1], f1, add);
+                            sc[2] = fmaf(sc[2], f0, add);
+                            sc[3] = fmaf(sc[3], f1, add);
+                            if (valid < tt * 16 + 16) {   // (columns without a query: nothing of theirs is used)
+                                sc[0] = (row0_ < n0) ? sc[0] : -INFINITY;
+                                sc[1] = (row0_ < n1) ? sc[1] : -INFINITY;
+                                sc[2] = (row8_ < n0) ? sc[2] : -INFINITY;
+                                sc[3] = (row8_ < n1) ? sc[3] : -INFINITY;
+                            }
                         } else {
                             const int tok0 = jb * BS + tt * 16 + (F16 ? tok_of_row(g) : g);
                             const int tok8 = jb * BS + tt * 16 + (F16 ? tok_of_row(g + 8) : g + 8);
@@ -1188,6 +1198,10 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(&empty[st]);
+                }
+                if (++st == S) {
+                    st = 0;
+                    turn ^= 1u;
                 }
             }
 
