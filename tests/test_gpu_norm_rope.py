@@ -56,6 +56,32 @@ def test_norm_rope(kind, T, Hq, Hkv, D, R, il):
     assert err.item() == 0
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T,Hq,Hkv,D,R,il", [(9001, 3, 1, 64, 64, False), (15000, 1, 1, 128, 64, True), (2501, 40, 8, 128, 128, False),
+                                             (1800, 70, 9, 64, 64, False), (3333, 5, 3, 128, 128, False)])
+def test_many_tokens(kind, T, Hq, Hkv, D, R, il):
+    """CTAs that take several sets of tokens, sets of several tokens, more rows than one pass holds."""
+    (q, k, v), (dq, dk, dv), (qw, kw), cs, pos = inputs(T, Hq, Hkv, D, R, kind, seed=8)
+    NB = T // 16 + 2
+    slots = torch.randperm(NB * 16, generator=torch.Generator().manual_seed(2))[:T]
+    slots[T // 2] = -1
+    kc = torch.zeros(NB, Hkv, 16, D, dtype=DT[kind], device="cuda")
+    vc = torch.zeros_like(kc)
+    qo, q2 = (torch.empty(T, Hq, D, dtype=DT[kind], device="cuda") for _ in range(2))
+    ko = torch.empty(T, Hkv, D, dtype=DT[kind], device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = (qw.cuda(), kw.cuda(), 1e-6, cs.cuda(), pos.cuda())
+    pkv.qk_norm_rope(qo, ko, dq, dk, *args, il, err)
+    pkv.qk_norm_rope_and_cache(q2, dq, dk, dv, *args, kc, vc, slots.cuda(), il, device_error=err)
+    close(qo, plain.norm_rope(q, qw, 1e-6, cs, pos, il), kind, "q")
+    close(ko, plain.norm_rope(k, kw, 1e-6, cs, pos, il), kind, "k")
+    assert torch.equal(qo, q2) and err.item() == 0
+    ok = slots >= 0
+    at = slots[ok].cuda()
+    assert torch.equal(kc[at // 16, :, at % 16], ko[ok.cuda()])
+    assert torch.equal(vc[at // 16, :, at % 16], dv[ok.cuda()])
+
+
 @pytest.mark.parametrize("kind,cache", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "e4m3"), ("f32", "e4m3"),
                                         ("bf16", "e5m2"), ("bf16", "int8"), ("f32", "int8")])
 @pytest.mark.parametrize("T,Hq,Hkv,D,R,BS,il", [(9, 8, 2, 128, 128, 16, False), (50, 5, 1, 64, 32, 8, True),
