@@ -451,7 +451,14 @@ int heads_impl(void* out, const void* q, const void* k_cache, const void* v_cach
             return st;
         if (occ < 1)
             return PKV_ERR_SHAPE;
-        runs = sms * (occ > kMaxRunsPerSM ? kMaxRunsPerSM : occ);
+        // A run leaves pieces of HG KV heads: with one, more runs fit the workspace of three an SM. They are
+        // used where a stream is not cut into more than about 16 pieces by them (7 streams: 34 us with
+        // 444 runs, 47 us with 1184, which a warp per column had to merge).
+        const long long streams = (long long)num_seqs * (num_kv_heads / HG);
+        const int most = HG == 1 ? kMaxRunsPerSM * kMaxHeadGroup : kMaxRunsPerSM;
+        runs = sms * (occ > most ? most : occ);
+        if (occ > kMaxRunsPerSM && runs > 16 * streams)
+            runs = 16 * streams > sms * kMaxRunsPerSM ? (int)(16 * streams) : sms * kMaxRunsPerSM;
         // Few units: four to a run, not one. A run's copies are in flight together, so more units cost it
         // little, while every run leaves a piece of each stream to merge (one sequence, 64 selected
         // blocks: 16.4 us with 32 runs, 21.5 us with 296).
@@ -462,12 +469,15 @@ int heads_impl(void* out, const void* q, const void* k_cache, const void* v_cach
             few = true;
         }
     }
+    // runs of four KV heads that need as much workspace (an explicit num_partitions is sized as given)
+    const int sized = num_partitions > 0 ? runs : (int)(((long long)runs * HG + kMaxHeadGroup - 1) / kMaxHeadGroup);
     DecodeParams p;
+    int prepared = 0;
     const int st = decode_prepare(out, q, k_cache, v_cache, block_tables, seq_lens, num_seqs, num_heads, num_kv_heads,
                                   head_dim, block_size, scale, max_blocks_per_seq, num_blocks, q_dtype, kv_dtype,
-                                  scaled ? 1.0f : k_scale, scaled ? 1.0f : v_scale, runs, workspace, workspace_bytes,
-                                  nullptr, -1, 1, nullptr, nullptr, &p, &runs);
-    if (st != PKV_OK || runs == 0)
+                                  scaled ? 1.0f : k_scale, scaled ? 1.0f : v_scale, sized, workspace, workspace_bytes,
+                                  nullptr, -1, 1, nullptr, nullptr, &p, &prepared);
+    if (st != PKV_OK || prepared == 0)
         return st;
     p.selected = selected;
     p.sel_width = num_selected;
@@ -475,7 +485,8 @@ int heads_impl(void* out, const void* q, const void* k_cache, const void* v_cach
     p.v_block_scales = v_block_scales;
     // (a grid of few runs ends as one: waiting for it beats polling its stamps: 15.7 us to the 16.4 us
     // above, and 16.4 to 18.5 us for eight sequences)
-    if (few || recorded(static_cast<cudaStream_t>(stream)))
+    // (and the workspace has stamps for `sized` runs)
+    if (few || sized < runs || recorded(static_cast<cudaStream_t>(stream)))
         p.chunk_done = nullptr;
     op = MmaOp{};
     op.kind = MmaOp::kLaunchPerHead;

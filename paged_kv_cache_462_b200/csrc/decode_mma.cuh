@@ -305,7 +305,16 @@ struct MmaCfg {
     static constexpr int kSide = PH ? HG * 16 : 0;            // a stage's UnitHead entries
     // CTAs per SM: E4M3 tiles (16 KB stages) take three, for 12 consumer warps per SM to hide the
     // widening chain's latency; the same ~192 KB of stages per SM stay in flight either way
-    static constexpr int kCtasPerSM = (KV::kBytes == 1 && kStage <= 16384) ? 3 : 2;
+    // (PH, 8-bit, one KV head to a unit: eight, as the registers allow, or an SM would have three consumer
+    // warps for a kernel that their latency bounds. 5 KV heads x 32 sequences of 4000-8192 tokens, E4M3,
+    // 92 -> 61 us; 1 x 64, 46 -> 35 us. Two heads to a unit or bf16 gained nothing by more.)
+    static constexpr int ctas_per_sm()
+    {
+        if (!PH || HG > 1 || KV::kBytes > 1)
+            return (KV::kBytes == 1 && kStage <= 16384) ? 3 : 2;
+        return 8;
+    }
+    static constexpr int kCtasPerSM = ctas_per_sm();
     static_assert(kRowBytes % 128 == 0, "rows are whole 128-byte swizzle spans");
     static_assert(BS % 16 == 0 && G <= 8 && HG <= 8, "tile shape");
     static_assert(kRows <= 256, "TMA box height");

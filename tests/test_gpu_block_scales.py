@@ -4,7 +4,11 @@ two), the decode is held to the 64-bit softmax.
 Decode tolerance, on the size A = sum p |v| of an output's terms: the output's rounding (bf16, 2^-8
 of the value), the weights' (f16, 2^-11), and what the scores are off: q is exact in f16 (E4M3 and
 E5M2), and for INT8 rounded to 2^-13 of its largest element, which moves a score by at most
-scale * sum |k_d| * max|q| * 2^-14 and a weight by twice that (its sum moves too)."""
+scale * sum |k_d| * max|q| * 2^-14 and a weight by twice that (its sum moves too).
+Weights below f16's smallest normal number are off by up to half its smallest step, 2^-25, whatever their
+size: with w = 2^(s + log2 vs - m) the kernel's weights, an output is sum w code / sum (w / vs), the largest
+w is at least 1, so the lower sum is at least 1 / vs of its block, and the output is off by at most
+2^-25 * max vs * sum |code|. (It shows where the token with all the weight holds a zero.)"""
 import itertools
 import math
 
@@ -162,6 +166,16 @@ def check_decode(lens, Hq, Hkv, block, kind, spread, partitions=(0,), selected=N
         ks, vs = torch.full_like(ks, one), torch.full_like(vs, one)
     want, size = plain.decode(q, plain.values(k), plain.values(v), table, lens, D ** -0.5, block, selected, ks, vs)
     room = 2.0 ** -8 * want.abs() + 2.0 ** -11 * size + 1e-5 * size
+    tiny = torch.zeros_like(want)
+    for s, L in enumerate(lens):
+        n = -(-L // block)
+        for h in range(Hkv):
+            js = list(range(n)) if selected is None else [j for j in selected[s][h][:n] if j >= 0]
+            if js:
+                ids = table[s, js].long()
+                codes = plain.values(v)[ids, h].abs().nan_to_num(0.0).sum((0, 1))
+                tiny[s, h * Hq // Hkv:(h + 1) * Hq // Hkv] = 2.0 ** -25 * float(vs[ids, h].max()) * codes
+    room = room + tiny
     if kind == "int8":
         big_k = float((plain.values(k).abs().sum(-1) * ks.double()[..., None]).max())
         room = room + 2 * (D ** -0.5) * big_k * float(q.abs().max()) * 2.0 ** -14 * size
@@ -260,3 +274,16 @@ def test_decode_captured_twice_on_one_stream():
         torch.cuda.synchronize()
         for (g, x, o), j in zip(graphs, (i, i + 1)):
             assert torch.equal(o, want[j])
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("Hq,Hkv,block", [(4, 1, 16), (15, 3, 16), (8, 1, 32)])
+def test_decode_many_sequences_of_few_heads(kind, Hq, Hkv, block):
+    """One KV head to a unit and enough streams for more than three runs an SM."""
+    lens = [(37 * i * i + 11) % 1100 for i in range(110)]
+    check_decode(lens, Hq, Hkv, block, kind, 1.0, (0,))
+    sel = [[[j for j in range(h, 60, 3)] + [-1] * 2 for h in range(Hkv)] for _ in lens]
+    width = max(len(r) for row in sel for r in row)
+    sel = [[(r + [-1] * width)[:width] for r in row] for row in sel]
+    sel = [[[j if j < -(-L // block) else -1 for j in r] for r in row] for row, L in zip(sel, lens)]
+    check_decode(lens, Hq, Hkv, block, kind, 1.0, (0,), selected=sel)
