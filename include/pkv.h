@@ -422,7 +422,8 @@ PKV_API int qk_norm_rope_and_cache(void* q_out, const void* q, const void* k, co
  *
  * paged_attention_decode_block_scales is paged_attention_decode over such a cache. Any positive
  * scales can be given, V scales within 2^-50 .. 2^50 (others are taken as the nearest of these).
- * Shapes as the tensor-core kernel's 8-bit ones (bf16 q, head_dim 128, block_size 16 or 32).
+ * Shapes as the tensor-core kernel's 8-bit ones (bf16 q, head_dim 128, block_size 16 or 32); q
+ * 16-byte aligned. pkv_set_fp8_kernel's choice does not apply.
  */
 PKV_API int reshape_and_cache_block_scales(const void* k, const void* v, void* k_cache, void* v_cache,
                                            float* k_block_scales, float* v_block_scales,
@@ -468,7 +469,8 @@ PKV_API int paged_attention_decode_block_scales(void* out, const void* q, const 
  * too; a block listed twice counts twice; a list without a token gives zero rows. Order does not
  * matter but for rounding. Scales: k_block_scales and v_block_scales (both, or null and k_scale,
  * v_scale) for 8-bit caches. Shapes as the tensor-core kernel's (bf16 q; bf16 caches with head_dim
- * 64 or 128, 8-bit ones with 128; block_size 16 or 32). Workspace as paged_attention_decode's.
+ * 64 or 128, 8-bit ones with 128; block_size 16 or 32); q 16-byte aligned. Workspace as
+ * paged_attention_decode's. pkv_set_fp8_kernel's choice does not apply.
  */
 PKV_API int update_key_bounds(void* key_bounds, const void* k_cache, const int32_t* block_tables,
                               const int32_t* seq_lens, const int32_t* row_offsets, int num_tokens, int num_seqs,

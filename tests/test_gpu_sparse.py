@@ -560,3 +560,36 @@ def test_the_binding_without_its_hot_path(monkeypatch):
     got = run()
     for a, b in zip(want, got):
         assert torch.equal(a, b)
+
+
+def test_streams_given_by_argument(monkeypatch):
+    """A stream that is not the current one: another stream's object, its handle, and the legacy default
+    stream from within a side stream; the kept workspaces are made on the stream that uses them."""
+    monkeypatch.setattr(pkv, "_op_ws", {})
+    gen = torch.Generator().manual_seed(61)
+    lens = [900, 33]
+    table, pool = plain.tables(lens, 16, gen)
+    b = bounds_like(pool, 2, 128, gen).cuda()
+    k = torch.randn(pool, 2, 16, 128, generator=gen).to(torch.bfloat16).cuda()
+    dt, sl = table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    q = torch.randn(2, 8, 128, generator=gen).to(torch.bfloat16).cuda()
+
+    def run(stream):
+        sel, out = torch.empty(2, 2, 9, dtype=torch.int32, device="cuda"), torch.empty_like(q)
+        torch.cuda.synchronize()
+        pkv.select_blocks(sel, q, b, dt, sl, 16, stream=stream)
+        pkv.paged_attention_decode_sparse(out, q, k, k, dt, sl, sel, 0.1, stream=stream)
+        torch.cuda.synchronize()
+        return sel, out
+
+    want = run(None)
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [run(side), run(side.cuda_stream)]
+    with torch.cuda.stream(other):
+        got += [run(None), run(0), run(side)]
+    for g in got:
+        assert torch.equal(g[0], want[0]) and torch.equal(g[1], want[1])
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(ValueError):                       # which stream's graph would hold the workspace?
+        with torch.cuda.graph(graph):
+            pkv.select_blocks(want[0], q, b, dt, sl, 16, stream=side)
