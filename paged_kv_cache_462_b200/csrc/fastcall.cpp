@@ -135,13 +135,9 @@ int code_of(at::ScalarType t)
 constexpr int kMaxSymbols = 16, kMaxEntries = 24;
 
 // pointers (one an entry), symbols in order of appearance, row strides, the code of X, the code of K,
-// the device
-PyObject* match(PyObject*, PyObject* const* args, Py_ssize_t n)
+// the device. Throws for tensors without a storage or with symbolic sizes (vmap's wrappers, fake tensors).
+PyObject* match_or_throw(PyObject* const* args, Py_ssize_t n)
 {
-    if (n < 1) {
-        PyErr_SetString(PyExc_TypeError, "match(spec, tensor, ...)");
-        return nullptr;
-    }
     const Spec* spec = static_cast<const Spec*>(PyCapsule_GetPointer(args[0], "pkv.spec"));
     if (!spec)
         return nullptr;
@@ -222,6 +218,8 @@ PyObject* match(PyObject*, PyObject* const* args, Py_ssize_t n)
             Py_RETURN_NONE;
         }
         ptr[e] = t.data_ptr();
+        if (!ptr[e] && t.numel() > 0)   // a fake tensor's
+            Py_RETURN_NONE;
     }
     for (int i = 0; i < spec->symbols; ++i)
         if (!bound[i])
@@ -254,6 +252,22 @@ PyObject* match(PyObject*, PyObject* const* args, Py_ssize_t n)
             return nullptr;
         }
     return out;
+}
+
+// No C++ exception may leave a function that Python calls: what throws is no match, and the caller's
+// own checks raise.
+PyObject* match(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    if (n < 1) {
+        PyErr_SetString(PyExc_TypeError, "match(spec, tensor, ...)");
+        return nullptr;
+    }
+    try {
+        return match_or_throw(args, n);
+    } catch (...) {
+        PyErr_Clear();
+        Py_RETURN_NONE;
+    }
 }
 
 // ------------------------------------------------------------------ calls
