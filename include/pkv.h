@@ -146,7 +146,10 @@ PKV_API int pkv_workspace_init(void* workspace, size_t workspace_bytes, void* st
  *                (ignored for F32/BF16 caches)
  *   workspace    device buffer of >= paged_attention_workspace_size(...,
  *                num_partitions) bytes, zeroed once by pkv_workspace_init;
- *                calls that share a workspace must not overlap on the GPU.
+ *                calls that share a workspace must not overlap on the GPU, nor be
+ *                issued by two threads at once, even to one stream: a call's two
+ *                launches hand over through the workspace, and no other call's may
+ *                come between them.
  */
 PKV_API int paged_attention_decode(void* out, const void* q, const void* k_cache, const void* v_cache,
                            const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
@@ -461,7 +464,8 @@ PKV_API int paged_attention_decode_block_scales(void* out, const void* q, const 
  * finite ranks first, one with a bad block id (PKV_DEVERR_BLOCK_ID) last. q is bf16. The
  * workspace (pkv_select_workspace_size bytes) starts zeroed (pkv_workspace_init) and holds the
  * error word; one can serve calls of any sizes it is large enough for, but calls that share one
- * must not overlap on the GPU. Two launches, in order on `stream`.
+ * must not overlap on the GPU, nor be issued by two threads at once, even to one stream. Two
+ * launches, in order on `stream`.
  *
  * paged_attention_decode_sparse attends, for KV head h of sequence s, the tokens of the listed
  * blocks only. Of a list the first min(num_selected, ceil(seq_lens[s] / block_size)) entries are

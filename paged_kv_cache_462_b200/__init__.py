@@ -24,6 +24,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 import torch
 
@@ -258,15 +259,17 @@ def paged_attention_decode(out, q, k_cache, v_cache, block_tables, seq_lens, sca
     8-bit ones with k_scale/v_scale);
     block_tables: int32 [num_seqs, max_blocks_per_seq]; seq_lens: int32 [num_seqs].
     """
-    args = _decode_args(out, q, k_cache, v_cache, block_tables, seq_lens, scale, k_scale, v_scale,
-                        num_partitions, workspace, stream)
-    st = load_library().paged_attention_decode(*args, _stream_handle(stream))
+    args, sizes, dev = _decode_args(out, q, k_cache, v_cache, block_tables, seq_lens, scale, k_scale, v_scale,
+                                    num_partitions)
+    with _workspace(workspace, sizes, num_partitions, dev, stream) as ws:
+        st = load_library().paged_attention_decode(*args, _cuda("workspace", ws, dev), ws.numel(),
+                                                   _stream_handle(stream))
     _check("paged_attention_decode", st)
 
 
-def _decode_args(out, q, k_cache, v_cache, block_tables, seq_lens, scale, k_scale, v_scale, num_partitions,
-                 workspace, stream=None):
-    """Checked C arguments of a decode call, up to (not including) the stream."""
+def _decode_args(out, q, k_cache, v_cache, block_tables, seq_lens, scale, k_scale, v_scale, num_partitions):
+    """Checked C arguments of a decode call, up to (not including) the workspace; the sizes that a
+    workspace depends on; the device."""
     dev = _launch_device("q", q)
     S, Hq, D = q.shape
     NB, Hkv, BS, D2 = k_cache.shape
@@ -278,13 +281,11 @@ def _decode_args(out, q, k_cache, v_cache, block_tables, seq_lens, scale, k_scal
         raise TypeError("block_tables and seq_lens must be int32")
     if block_tables.dim() != 2 or block_tables.shape[0] != S or seq_lens.shape != (S,):
         raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
-    if workspace is None:
-        workspace = _cached_workspace(S, Hq, Hkv, D, num_partitions, dev, stream)
-    return (_cuda("out", out, dev), _cuda("q", q, dev), _cuda("k_cache", k_cache, dev),
-            _cuda("v_cache", v_cache, dev), _cuda("block_tables", block_tables, dev),
-            _cuda("seq_lens", seq_lens, dev), S, Hq, Hkv, D, BS, float(scale),
-            block_tables.shape[1], NB, _dtype_code(q), _dtype_code(k_cache), float(k_scale), float(v_scale),
-            int(num_partitions), _cuda("workspace", workspace, dev), workspace.numel())
+    return ((_cuda("out", out, dev), _cuda("q", q, dev), _cuda("k_cache", k_cache, dev),
+             _cuda("v_cache", v_cache, dev), _cuda("block_tables", block_tables, dev),
+             _cuda("seq_lens", seq_lens, dev), S, Hq, Hkv, D, BS, float(scale),
+             block_tables.shape[1], NB, _dtype_code(q), _dtype_code(k_cache), float(k_scale), float(v_scale),
+             int(num_partitions)), (S, Hq, Hkv, D), dev)
 
 
 def paged_attention_decode_mq(out, q, k_cache, v_cache, block_tables, seq_lens, scale, k_scale=1.0, v_scale=1.0,
@@ -303,14 +304,13 @@ def paged_attention_decode_mq(out, q, k_cache, v_cache, block_tables, seq_lens, 
         raise TypeError("block_tables and seq_lens must be int32")
     if block_tables.dim() != 2 or block_tables.shape[0] != S or seq_lens.shape != (S,):
         raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
-    if workspace is None:
-        workspace = _cached_workspace(S, Hq * QL, Hkv, D, num_partitions, dev, stream)
-    st = load_library().paged_attention_decode_mq(
-        _cuda("out", out, dev), _cuda("q", q, dev), _cuda("k_cache", k_cache, dev), _cuda("v_cache", v_cache, dev),
-        _cuda("block_tables", block_tables, dev), _cuda("seq_lens", seq_lens, dev), S, QL, Hq, Hkv, D, BS,
-        float(scale), block_tables.shape[1], NB, _dtype_code(q), _dtype_code(k_cache), float(k_scale),
-        float(v_scale), int(num_partitions), _cuda("workspace", workspace, dev), workspace.numel(),
-        _stream_handle(stream))
+    with _workspace(workspace, (S, Hq * QL, Hkv, D), num_partitions, dev, stream) as ws:
+        st = load_library().paged_attention_decode_mq(
+            _cuda("out", out, dev), _cuda("q", q, dev), _cuda("k_cache", k_cache, dev),
+            _cuda("v_cache", v_cache, dev), _cuda("block_tables", block_tables, dev),
+            _cuda("seq_lens", seq_lens, dev), S, QL, Hq, Hkv, D, BS, float(scale), block_tables.shape[1], NB,
+            _dtype_code(q), _dtype_code(k_cache), float(k_scale), float(v_scale), int(num_partitions),
+            _cuda("workspace", ws, dev), ws.numel(), _stream_handle(stream))
     _check("paged_attention_decode_mq", st)
 
 
@@ -319,9 +319,10 @@ def withheld_unit_decode(out, q, k_cache, v_cache, block_tables, seq_lens, scale
     """Failure-path test hook: paged_attention_decode with unit `withheld_unit`'s stage never handed
     to its consumers, so their bounded wait runs out and the workspace error word gets
     DEVERR_TIMEOUT (read it with read_device_error, then workspace_init before reuse)."""
-    args = _decode_args(out, q, k_cache, v_cache, block_tables, seq_lens, scale, k_scale, v_scale,
-                        num_partitions, workspace, stream)
-    st = load_library().pkv_test_decode_timeout(*args, int(withheld_unit), _stream_handle(stream))
+    args, _, dev = _decode_args(out, q, k_cache, v_cache, block_tables, seq_lens, scale, k_scale, v_scale,
+                                num_partitions)
+    st = load_library().pkv_test_decode_timeout(*args, _cuda("workspace", workspace, dev), workspace.numel(),
+                                                int(withheld_unit), _stream_handle(stream))
     _check("pkv_test_decode_timeout", st)
 
 
@@ -343,15 +344,14 @@ def paged_decode_step(out, q, k_cache, v_cache, block_tables, seq_lens, new_k, n
         raise TypeError("block_tables and seq_lens must be int32")
     if block_tables.dim() != 2 or block_tables.shape[0] != S or seq_lens.shape != (S,):
         raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
-    if workspace is None:
-        workspace = _cached_workspace(S, Hq, Hkv, D, num_partitions, dev, stream)
-    st = load_library().paged_decode_step(
-        _cuda("out", out, dev), _cuda("q", q, dev), _cuda("k_cache", k_cache, dev), _cuda("v_cache", v_cache, dev),
-        _cuda("block_tables", block_tables, dev), _cuda("seq_lens", seq_lens, dev), S, Hq, Hkv, D, BS,
-        float(scale), block_tables.shape[1], NB, _dtype_code(q), _dtype_code(k_cache), float(k_scale),
-        float(v_scale), int(num_partitions), _cuda("workspace", workspace, dev), workspace.numel(),
-        _cuda("new_k", new_k, dev), _cuda("new_v", new_v, dev), _cuda("slot_mapping", slot_mapping, dev),
-        _dtype_code(new_k), _stream_handle(stream))
+    with _workspace(workspace, (S, Hq, Hkv, D), num_partitions, dev, stream) as ws:
+        st = load_library().paged_decode_step(
+            _cuda("out", out, dev), _cuda("q", q, dev), _cuda("k_cache", k_cache, dev),
+            _cuda("v_cache", v_cache, dev), _cuda("block_tables", block_tables, dev),
+            _cuda("seq_lens", seq_lens, dev), S, Hq, Hkv, D, BS, float(scale), block_tables.shape[1], NB,
+            _dtype_code(q), _dtype_code(k_cache), float(k_scale), float(v_scale), int(num_partitions),
+            _cuda("workspace", ws, dev), ws.numel(), _cuda("new_k", new_k, dev), _cuda("new_v", new_v, dev),
+            _cuda("slot_mapping", slot_mapping, dev), _dtype_code(new_k), _stream_handle(stream))
     _check("paged_decode_step", st)
 
 
@@ -401,12 +401,13 @@ def reshape_and_cache_head_scales(k, v, k_cache, v_cache, slot_mapping, k_head_s
 def paged_attention_decode_head_scales(out, q, k_cache, v_cache, block_tables, seq_lens, scale, k_head_scales,
                                        v_head_scales, num_partitions=0, workspace=None, stream=None) -> None:
     """paged_attention_decode over an 8-bit cache with one scale per KV head."""
-    args = list(_decode_args(out, q, k_cache, v_cache, block_tables, seq_lens, scale, 1.0, 1.0, num_partitions,
-                             workspace, stream))
-    Hkv, dev = k_cache.shape[1], _launch_device("q", q)
-    args[16:18] = [_head_scales("k_head_scales", k_head_scales, Hkv, dev),
-                   _head_scales("v_head_scales", v_head_scales, Hkv, dev)]
-    st = load_library().paged_attention_decode_head_scales(*args, _stream_handle(stream))
+    args, sizes, dev = _decode_args(out, q, k_cache, v_cache, block_tables, seq_lens, scale, 1.0, 1.0, num_partitions)
+    Hkv = k_cache.shape[1]
+    args = (*args[:16], _head_scales("k_head_scales", k_head_scales, Hkv, dev),
+            _head_scales("v_head_scales", v_head_scales, Hkv, dev), *args[18:])
+    with _workspace(workspace, sizes, num_partitions, dev, stream) as ws:
+        st = load_library().paged_attention_decode_head_scales(*args, _cuda("workspace", ws, dev), ws.numel(),
+                                                               _stream_handle(stream))
     _check("paged_attention_decode_head_scales", st)
 
 
@@ -740,11 +741,11 @@ def paged_attention_decode_block_scales(out, q, k_cache, v_cache, block_tables, 
         vs = _block_scales("v_block_scales", v_block_scales, cache, dev)
         dt, kdt = _dtype_code(q), _dtype_code(k_cache)
     st = _raw_stream(stream, dev)
-    if workspace is None:
-        workspace = _op_workspace("decode", _sized(workspace_size, dev, S, Hq, Hkv, D, num_partitions), dev, st)
-    _check("paged_attention_decode_block_scales", load_library().paged_attention_decode_block_scales(
-        op, qp, kp, vp, bt, sl, S, Hq, Hkv, D, BS, float(scale), MB, NB, dt, kdt, ks, vs, int(num_partitions),
-        _ptr("workspace", workspace, dev), workspace.numel(), st))
+    n = 0 if workspace is not None else _sized(workspace_size, dev, S, Hq, Hkv, D, num_partitions)
+    with _op_workspace(workspace, "decode", n, dev, st) as ws:
+        _check("paged_attention_decode_block_scales", load_library().paged_attention_decode_block_scales(
+            op, qp, kp, vp, bt, sl, S, Hq, Hkv, D, BS, float(scale), MB, NB, dt, kdt, ks, vs, int(num_partitions),
+            _ptr("workspace", ws, dev), ws.numel(), st))
 
 
 def update_key_bounds(key_bounds, k_cache, block_tables, seq_lens, row_offsets, num_tokens, k_scale=1.0,
@@ -807,11 +808,11 @@ def select_blocks(selected, q, key_bounds, block_tables, seq_lens, block_size, n
             raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
         sel, qp, kb = _ptr("selected", selected, dev), _ptr("q", q, dev), _ptr("key_bounds", key_bounds, dev)
     st = _raw_stream(stream, dev)
-    if workspace is None:
-        workspace = _op_workspace("select", _sized(select_workspace_size, dev, S, Hkv, max(1, MB)), dev, st)
-    _check("select_blocks", load_library().select_blocks(
-        sel, qp, kb, bt, sl, S, Hq, Hkv, D, int(block_size), MB, NB, W, int(num_sink_blocks), int(num_recent_blocks),
-        _ptr("workspace", workspace, dev), workspace.numel(), st))
+    n = 0 if workspace is not None else _sized(select_workspace_size, dev, S, Hkv, max(1, MB))
+    with _op_workspace(workspace, "select", n, dev, st) as ws:
+        _check("select_blocks", load_library().select_blocks(
+            sel, qp, kb, bt, sl, S, Hq, Hkv, D, int(block_size), MB, NB, W, int(num_sink_blocks),
+            int(num_recent_blocks), _ptr("workspace", ws, dev), ws.numel(), st))
 
 
 def _selected_width(selected, S, Hkv) -> int:
@@ -844,12 +845,11 @@ def paged_attention_decode_sparse(out, q, k_cache, v_cache, block_tables, seq_le
             vs = _block_scales("v_block_scales", v_block_scales, cache, dev)
         sel, dt, kdt = _ptr("selected", selected, dev), _dtype_code(q), _dtype_code(k_cache)
     st = _raw_stream(stream, dev)
-    if workspace is None:
-        workspace = _op_workspace("decode", _sized(workspace_size, dev, S, Hq, Hkv, D, num_partitions), dev, st)
-    _check("paged_attention_decode_sparse", load_library().paged_attention_decode_sparse(
-        op, qp, kp, vp, bt, sl, sel, S, Hq, Hkv, D, BS, float(scale), MB, NB, W, dt, kdt, float(k_scale),
-        float(v_scale), ks or None, vs or None, int(num_partitions), _ptr("workspace", workspace, dev),
-        workspace.numel(), st))
+    n = 0 if workspace is not None else _sized(workspace_size, dev, S, Hq, Hkv, D, num_partitions)
+    with _op_workspace(workspace, "decode", n, dev, st) as ws:
+        _check("paged_attention_decode_sparse", load_library().paged_attention_decode_sparse(
+            op, qp, kp, vp, bt, sl, sel, S, Hq, Hkv, D, BS, float(scale), MB, NB, W, dt, kdt, float(k_scale),
+            float(v_scale), ks or None, vs or None, int(num_partitions), _ptr("workspace", ws, dev), ws.numel(), st))
 
 
 _sizes: dict = {}
@@ -865,46 +865,98 @@ def _sized(size, dev, *args) -> int:
     return n
 
 
+class _Kept:
+    """A workspace that the binding keeps for one stream, and its lock: a call holds it from the choice of the
+    workspace until its launches are queued. They are two that hand over through the workspace, and the
+    C call lets other threads run: their launches on the same stream would go in between."""
+    __slots__ = ("tensor", "lock")
+
+    def __init__(self):
+        self.tensor = None
+        self.lock = threading.RLock()
+
+    def __enter__(self):
+        return self.tensor
+
+    def __exit__(self, *_):
+        self.lock.release()
+
+
+class _Given:
+    """A workspace that one call alone uses, or that its caller answers for."""
+    __slots__ = ("tensor",)
+
+    def __init__(self, tensor):
+        self.tensor = tensor
+
+    def __enter__(self):
+        return self.tensor
+
+    def __exit__(self, *_):
+        pass
+
+
+def _hold(table, key, n, new, *args) -> _Kept:
+    """The workspace of at least n bytes that `table` keeps under `key`, its lock taken (``with`` gives the
+    tensor and frees the lock); new(n, old, *args) makes one."""
+    kept = table.get(key)
+    if kept is None:
+        kept = table.setdefault(key, _Kept())
+    kept.lock.acquire()
+    try:
+        if kept.tensor is None or kept.tensor.numel() < n:
+            kept.tensor = new(n, kept.tensor, *args)
+    except BaseException:
+        kept.lock.release()
+        raise
+    return kept
+
+
 _op_ws: dict = {}
 _OP_HEADER = 256     # what an operator's workspace needs cleared before its first call
 
 
-def _op_workspace(kind, n, dev, stream):
-    """A workspace of at least n bytes with a clear header, kept per (kind, device, stream), so that
-    calls on different streams never share one. It is allocated and cleared on the stream that uses
-    it. While that stream is being captured every call gets its own, from the graph's memory and
-    cleared inside the graph: two graphs, or a graph and later eager calls, never meet in one."""
-    capturing = torch.cuda.is_current_stream_capturing()
-    if capturing and stream != _current_raw_stream(dev):
-        raise ValueError("pass a workspace to capture on another stream than the current one")
-    ws = None if capturing else _op_ws.get((kind, dev, stream))
-    if ws is None or ws.numel() < n:
-        here = stream == _current_raw_stream(dev)
-        with torch.cuda.stream(torch.cuda.current_stream() if here else torch.cuda.ExternalStream(stream, device=dev)):
-            ws = torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", dev))
-        _check("pkv_workspace_init", load_library().pkv_workspace_init(_ptr("workspace", ws, dev), min(n, _OP_HEADER),
-                                                                       stream))
-        if not capturing:
-            _op_ws[(kind, dev, stream)] = ws
+def _op_workspace(workspace, kind, n, dev, stream):
+    """The caller's workspace, or one of at least n bytes with a clear header, kept per (kind, device,
+    stream), so that calls on different streams never share one. It is allocated and cleared on the
+    stream that uses it. While that stream is being captured every call gets its own, from the
+    graph's memory and cleared inside the graph: two graphs, or a graph and later eager calls, never
+    meet in one."""
+    if workspace is not None:
+        return _Given(workspace)
+    if torch.cuda.is_current_stream_capturing():
+        if stream != _current_raw_stream(dev):
+            raise ValueError("pass a workspace to capture on another stream than the current one")
+        return _Given(_new_op_workspace(n, None, dev, stream))
+    return _hold(_op_ws, (kind, dev, stream), n, _new_op_workspace, dev, stream)
+
+
+def _new_op_workspace(n, _, dev, stream):
+    here = stream == _current_raw_stream(dev)
+    with torch.cuda.stream(torch.cuda.current_stream() if here else torch.cuda.ExternalStream(stream, device=dev)):
+        ws = torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", dev))
+    _check("pkv_workspace_init", load_library().pkv_workspace_init(_ptr("workspace", ws, dev), min(n, _OP_HEADER),
+                                                                   stream))
     return ws
 
 
 _ws_cache: dict = {}
 
 
-def _cached_workspace(S, Hq, Hkv, D, parts, dev, stream):
-    """A workspace kept per (device, partitions, stream), so calls on different streams never share
-    one; a new one is zeroed by the library on the stream that will use it."""
-    n = workspace_size(S, Hq, Hkv, D, parts)
+def _workspace(workspace, sizes, parts, dev, stream):
+    """The caller's workspace, or one kept per (device, partitions, stream), so calls on different streams
+    never share one; a new one is zeroed by the library on the stream that will use it."""
+    if workspace is not None:
+        return _Given(workspace)
     handle = _stream_handle(stream)
-    key = (dev, parts, handle.value)
-    ws = _ws_cache.get(key)
-    if ws is None or ws.numel() < n:
-        if ws is not None:
-            torch.cuda.synchronize(dev)   # the smaller one may still be in use on its stream
-        ws = torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", dev))
-        _check("pkv_workspace_init", load_library().pkv_workspace_init(_cuda("workspace", ws), n, handle))
-        _ws_cache[key] = ws
+    return _hold(_ws_cache, (dev, parts, handle.value), workspace_size(*sizes, parts), _new_workspace, dev, handle)
+
+
+def _new_workspace(n, old, dev, handle):
+    if old is not None:
+        torch.cuda.synchronize(dev)   # the smaller one may still be in use on its stream
+    ws = torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", dev))
+    _check("pkv_workspace_init", load_library().pkv_workspace_init(_cuda("workspace", ws), n, handle))
     return ws
 
 
