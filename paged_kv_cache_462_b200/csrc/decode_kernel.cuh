@@ -635,6 +635,13 @@ struct DecodeLauncher {
         // E4M3 codes are widened to fp32 with a 2^-120 bias (see device.cuh): fold 2^120 into the scales
         p.q_scale = p.scale * kLog2e * (KV::kBytes == 1 ? p.k_scale * KV::kUnbias : 1.0f);
         p.v_scale = KV::kBytes == 1 ? p.v_scale_in * KV::kUnbias : 1.0f;
+        // The first 64 arrival counters lie where no workspace layout has anything else. Behind them a call
+        // of other sizes may have left its stamps or partials, so they are cleared before each launch
+        // (a memset of a few KB, from 65 (sequence, KV head) pairs on).
+        const long long pairs = (long long)p.num_seqs * p.num_kv_heads;
+        if (pairs > kCountersAlone &&
+            cudaMemsetAsync(p.counters + kCountersAlone, 0, (size_t)(pairs - kCountersAlone) * 4, stream) != cudaSuccess)
+            return PKV_ERR_LAUNCH;
         kern<<<nruns, C::kThreads, smem, stream>>>(p);
         return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_LAUNCH;
     }

@@ -14,6 +14,7 @@ constexpr int kMaxSmemPerBlock = 227 * 1024;
 constexpr int kMaxSeqs = 16384;         // per call: the per-sequence tile prefix lives in shared memory
 constexpr int kMaxRunsPerSM = 3;        // automatic partition count is at most 3 runs per SM
 constexpr size_t kWorkspaceHeader = 256;
+constexpr int kCountersAlone = 64;       // arrival counters that every workspace layout has behind the header
 constexpr int kMaxHeadGroup = 4;        // KV heads per MMA work unit (partial slots reserved per run)
 // Tensor-core kernels: a CTA's first chunk is its share of three quarters of the work; the last
 // quarter is cut into up to kTailChunksPerRun chunks per CTA, claimed as CTAs run dry. The
@@ -44,7 +45,7 @@ struct DecodeParams {
     float q_scale;     // set by the launcher: factor applied to q.K to get log2-domain scores
     float v_scale;     // set by the launcher: factor applied to the output
     int32_t* err;      // workspace error word
-    int32_t* counters; // [num_seqs * num_kv_heads] arrivals, zero between calls
+    int32_t* counters; // [num_seqs * num_kv_heads] arrivals; the first kCountersAlone are zero between calls
     float* partials;   // [(runs + pairs)][slot_floats]
     int slot_floats;
     int stages_per_warp; // set by the launcher
