@@ -522,6 +522,13 @@ PKV_API int pkv_validate_tables(const int32_t* block_tables, const int32_t* seq_
                                 int max_blocks_per_seq, int block_size, int num_blocks,
                                 const int64_t* slot_mapping, int32_t* bad_bits, int32_t* first_bad);
 
+/*
+ * 1 while launches on `stream` are being recorded into a graph, else 0. A workspace
+ * that such a call uses stays in the graph: it has to live as long, and calls that
+ * run beside a replay must not share it.
+ */
+PKV_API int pkv_stream_recorded(void* stream);
+
 /* Number of partitions num_partitions = 0 resolves to for this configuration on the current device. */
 PKV_API int pkv_default_partitions(int head_dim, int block_size, int num_heads, int num_kv_heads, int kv_dtype);
 

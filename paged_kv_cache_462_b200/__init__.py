@@ -120,6 +120,8 @@ def load_library():
     lib.pkv_validate_tables.argtypes = [P, P, i32, i32, i32, i32, P, ctypes.POINTER(ctypes.c_int32),
                                         ctypes.POINTER(ctypes.c_int32)]
     lib.pkv_validate_tables.restype = i32
+    lib.pkv_stream_recorded.argtypes = [P]
+    lib.pkv_stream_recorded.restype = i32
     lib.pkv_status_string.argtypes = [i32]
     lib.pkv_status_string.restype = ctypes.c_char_p
     _bind_fast(lib)
@@ -142,7 +144,7 @@ def _bind_fast(lib) -> None:
         return
     for name in ("qk_norm_rope", "qk_norm_rope_and_cache", "reshape_and_cache_block_scales",
                  "paged_attention_decode_block_scales", "update_key_bounds", "select_blocks",
-                 "paged_attention_decode_sparse"):
+                 "paged_attention_decode_sparse", "pkv_stream_recorded"):
         _fastcall.bind(name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value)
         setattr(lib, name, getattr(_fastcall, name))
     caches = "k_cache:N,Hkv,B,D:c:K v_cache:N,Hkv,B,D:c:K"
@@ -912,6 +914,17 @@ def _hold(table, key, n, new, *args) -> _Kept:
     return kept
 
 
+def _recorded(stream, current) -> bool:
+    """Whether calls on `stream` are being recorded into a graph. If either it or the current stream is, but not
+    both as one, a workspace could come from the wrong place: memory of the graph that eager calls
+    keep, or kept memory that the graph would go on using after a larger workspace has replaced it."""
+    recorded = load_library().pkv_stream_recorded
+    here = recorded(current) != 0
+    if stream != current and (here or recorded(stream) != 0):
+        raise ValueError("pass a workspace to capture on another stream than the current one")
+    return here
+
+
 _op_ws: dict = {}
 _OP_HEADER = 256     # what an operator's workspace needs cleared before its first call
 
@@ -924,9 +937,7 @@ def _op_workspace(workspace, kind, n, dev, stream):
     meet in one."""
     if workspace is not None:
         return _Given(workspace)
-    if torch.cuda.is_current_stream_capturing():
-        if stream != _current_raw_stream(dev):
-            raise ValueError("pass a workspace to capture on another stream than the current one")
+    if _recorded(stream, _current_raw_stream(dev)):
         return _Given(_new_op_workspace(n, None, dev, stream))
     return _hold(_op_ws, (kind, dev, stream), n, _new_op_workspace, dev, stream)
 

@@ -354,6 +354,8 @@ int pkv_read_device_error(void* workspace, size_t workspace_bytes, int32_t* host
     return PKV_OK;
 }
 
+int pkv_stream_recorded(void* stream) { return recorded(static_cast<cudaStream_t>(stream)) ? 1 : 0; }
+
 int pkv_default_partitions(int head_dim, int block_size, int num_heads, int num_kv_heads, int kv_dtype)
 {
     if (num_kv_heads <= 0 || num_heads % num_kv_heads != 0)

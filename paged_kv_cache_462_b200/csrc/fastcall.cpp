@@ -343,6 +343,7 @@ PKV_FAST(paged_attention_decode_block_scales)
 PKV_FAST(update_key_bounds)
 PKV_FAST(select_blocks)
 PKV_FAST(paged_attention_decode_sparse)
+PKV_FAST(pkv_stream_recorded)
 #undef PKV_FAST
 
 // bind(name, address): the module's function `name` calls the C function at `address` from here on.
@@ -364,6 +365,7 @@ PyObject* bind(PyObject*, PyObject* args)
     PKV_BIND(update_key_bounds)
     PKV_BIND(select_blocks)
     PKV_BIND(paged_attention_decode_sparse)
+    PKV_BIND(pkv_stream_recorded)
 #undef PKV_BIND
     Py_RETURN_FALSE;
 }
@@ -380,6 +382,7 @@ PyMethodDef methods[] = {
     PKV_METHOD(update_key_bounds),
     PKV_METHOD(select_blocks),
     PKV_METHOD(paged_attention_decode_sparse),
+    PKV_METHOD(pkv_stream_recorded),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", "Hot path of the binding.", -1, methods,
