@@ -926,7 +926,7 @@ def _recorded(stream, current) -> bool:
 
 
 _op_ws: dict = {}
-_OP_HEADER = 256     # what an operator's workspace needs cleared before its first call
+_HEADER = 512        # what a workspace needs cleared before its first call: header and first arrival counters
 
 
 def _op_workspace(workspace, kind, n, dev, stream):
@@ -946,7 +946,7 @@ def _new_op_workspace(n, _, dev, stream):
     here = stream == _current_raw_stream(dev)
     with torch.cuda.stream(torch.cuda.current_stream() if here else torch.cuda.ExternalStream(stream, device=dev)):
         ws = torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", dev))
-    _check("pkv_workspace_init", load_library().pkv_workspace_init(_ptr("workspace", ws, dev), min(n, _OP_HEADER),
+    _check("pkv_workspace_init", load_library().pkv_workspace_init(_ptr("workspace", ws, dev), min(n, _HEADER),
                                                                    stream))
     return ws
 
@@ -956,11 +956,14 @@ _ws_cache: dict = {}
 
 def _workspace(workspace, sizes, parts, dev, stream):
     """The caller's workspace, or one kept per (device, partitions, stream), so calls on different streams
-    never share one; a new one is zeroed by the library on the stream that will use it."""
+    never share one; a new one is zeroed by the library on the stream that will use it. While that
+    stream is being captured every call gets its own, as in _op_workspace."""
     if workspace is not None:
         return _Given(workspace)
-    handle = _stream_handle(stream)
-    return _hold(_ws_cache, (dev, parts, handle.value), workspace_size(*sizes, parts), _new_workspace, dev, handle)
+    handle, n = _stream_handle(stream), workspace_size(*sizes, parts)
+    if _recorded(handle.value or 0, torch.cuda.current_stream().cuda_stream):
+        return _Given(_new_op_workspace(n, None, dev, handle.value or 0))
+    return _hold(_ws_cache, (dev, parts, handle.value), n, _new_workspace, dev, handle)
 
 
 def _new_workspace(n, old, dev, handle):

@@ -79,3 +79,57 @@ def test_a_captured_stream_given_by_argument():
             pkv.select_blocks(sel, q, kb, t, sl, 16, workspace=ws, stream=side)
     graph.replay()
     assert torch.equal(sel, want)
+
+
+DENSE = ("decode", "step", "mq", "head_scales")
+
+
+@pytest.mark.parametrize("name", DENSE)
+@pytest.mark.parametrize("captured", [{7}, {0}])
+def test_dense_calls_on_another_stream(lib, monkeypatch, name, captured):
+    call = streamed(name, monkeypatch, 7)
+    lib.captured |= captured
+    with pytest.raises(ValueError, match="pass a workspace"):
+        call()
+    assert not launched(lib) and not pkv._ws_cache
+
+
+@pytest.mark.parametrize("name", DENSE)
+def test_dense_calls_on_the_current_stream(lib, name):
+    call = calls()[name]
+    lib.captured.add(0)
+    call(), call()
+    assert not pkv._ws_cache
+    assert len([c for c in lib.calls if c[0] == "pkv_workspace_init"]) == 2
+    lib.captured.clear()
+    call()
+    assert len(pkv._ws_cache) == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,Hkv", [(torch.bfloat16, 2), (torch.float32, 16)])
+def test_a_dense_decode_captured_without_a_workspace(dtype, Hkv):
+    """The first call on the stream is a captured one; then larger eager calls; then replays with other queries."""
+    S, Hq, D, L = 6, 16, 128 if dtype == torch.bfloat16 else 64, 2000
+    n = -(-L // 16)
+    t = torch.randperm(S * n, device="cuda").to(torch.int32).reshape(S, n)
+    k, v = (torch.randn(S * n, Hkv, 16, D, device="cuda").to(dtype) for _ in range(2))
+    sl = torch.full((S,), L, dtype=torch.int32, device="cuda")
+    q = torch.randn(S, Hq, D, device="cuda").to(dtype)
+    out = torch.empty_like(q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        pkv.paged_attention_decode(out, q, k, v, t, sl, 0.1)
+    big = [x.repeat(8, *[1] * (x.dim() - 1)) for x in (q, t, sl)]
+    for i in range(3):
+        q.normal_()
+        want, wide = torch.empty_like(q), torch.empty_like(big[0])
+        with torch.cuda.stream(side):
+            side.wait_stream(torch.cuda.default_stream())
+            pkv.paged_attention_decode(wide, big[0], k, v, big[1], big[2], 0.1)
+            pkv.paged_attention_decode(want, q, k, v, t, sl, 0.1)
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
