@@ -467,11 +467,9 @@ def _plan_args(plan: DevicePrefixPlan, dev, S, MB):
             ptr("plan.lens", plan.lens), _cuda("plan.shared", plan.shared, dev), plan.num_groups, plan.max_group)
 
 
-def _shared_prefix_workspace(workspace, S, Hq, Hkv, D, plan, num_partitions, dev):
-    if workspace is not None:
-        return workspace
-    n = shared_prefix_workspace_size(S, Hq, Hkv, D, plan.num_groups, num_partitions)
-    return torch.zeros(n, dtype=torch.uint8, device=torch.device("cuda", dev))
+def _shared_prefix_workspace(workspace, S, Hq, Hkv, D, plan, num_partitions, dev, stream):
+    n = 0 if workspace is not None else shared_prefix_workspace_size(S, Hq, Hkv, D, plan.num_groups, num_partitions)
+    return _op_workspace(workspace, "shared_prefix", n, dev, _raw_stream(stream, dev))
 
 
 def paged_attention_decode_shared_prefix(out, q, k_cache, v_cache, block_tables, seq_lens, plan, scale,
@@ -487,13 +485,14 @@ def paged_attention_decode_shared_prefix(out, q, k_cache, v_cache, block_tables,
     if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32 or block_tables.dim() != 2 \
             or block_tables.shape[0] != S or seq_lens.shape != (S,):
         raise ValueError("block_tables must be int32 [num_seqs, max_blocks] and seq_lens int32 [num_seqs]")
-    ws = _shared_prefix_workspace(workspace, S, Hq, Hkv, D, plan, num_partitions, dev)
-    st = load_library().paged_attention_decode_shared_prefix(
-        _cuda("out", out, dev), _cuda("q", q, dev), _cuda("k_cache", k_cache, dev), _cuda("v_cache", v_cache, dev),
-        _cuda("block_tables", block_tables, dev), _cuda("seq_lens", seq_lens, dev), S, Hq, Hkv, D, BS,
-        float(scale), block_tables.shape[1], NB, _dtype_code(q), _dtype_code(k_cache), float(k_scale),
-        float(v_scale), *_plan_args(plan, dev, S, block_tables.shape[1]), int(num_partitions),
-        _cuda("workspace", ws, dev), ws.numel(), _stream_handle(stream))
+    with _shared_prefix_workspace(workspace, S, Hq, Hkv, D, plan, num_partitions, dev, stream) as ws:
+        st = load_library().paged_attention_decode_shared_prefix(
+            _cuda("out", out, dev), _cuda("q", q, dev), _cuda("k_cache", k_cache, dev),
+            _cuda("v_cache", v_cache, dev), _cuda("block_tables", block_tables, dev),
+            _cuda("seq_lens", seq_lens, dev), S, Hq, Hkv, D, BS, float(scale), block_tables.shape[1], NB,
+            _dtype_code(q), _dtype_code(k_cache), float(k_scale), float(v_scale),
+            *_plan_args(plan, dev, S, block_tables.shape[1]), int(num_partitions), _cuda("workspace", ws, dev),
+            ws.numel(), _stream_handle(stream))
     _check("paged_attention_decode_shared_prefix", st)
 
 
@@ -513,14 +512,15 @@ def paged_decode_step_shared_prefix(out, q, k_cache, v_cache, block_tables, seq_
         raise ValueError("new_k/new_v must be [num_seqs, num_kv_heads, head_dim] of one dtype")
     if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (S,):
         raise TypeError("slot_mapping must be int64 [num_seqs]")
-    ws = _shared_prefix_workspace(workspace, S, Hq, Hkv, D, plan, num_partitions, dev)
-    st = load_library().paged_decode_step_shared_prefix(
-        _cuda("out", out, dev), _cuda("q", q, dev), _cuda("k_cache", k_cache, dev), _cuda("v_cache", v_cache, dev),
-        _cuda("block_tables", block_tables, dev), _cuda("seq_lens", seq_lens, dev), S, Hq, Hkv, D, BS,
-        float(scale), block_tables.shape[1], NB, _dtype_code(q), _dtype_code(k_cache), float(k_scale),
-        float(v_scale), *_plan_args(plan, dev, S, block_tables.shape[1]), int(num_partitions),
-        _cuda("workspace", ws, dev), ws.numel(), _cuda("new_k", new_k, dev), _cuda("new_v", new_v, dev),
-        _cuda("slot_mapping", slot_mapping, dev), _dtype_code(new_k), _stream_handle(stream))
+    with _shared_prefix_workspace(workspace, S, Hq, Hkv, D, plan, num_partitions, dev, stream) as ws:
+        st = load_library().paged_decode_step_shared_prefix(
+            _cuda("out", out, dev), _cuda("q", q, dev), _cuda("k_cache", k_cache, dev),
+            _cuda("v_cache", v_cache, dev), _cuda("block_tables", block_tables, dev),
+            _cuda("seq_lens", seq_lens, dev), S, Hq, Hkv, D, BS, float(scale), block_tables.shape[1], NB,
+            _dtype_code(q), _dtype_code(k_cache), float(k_scale), float(v_scale),
+            *_plan_args(plan, dev, S, block_tables.shape[1]), int(num_partitions), _cuda("workspace", ws, dev),
+            ws.numel(), _cuda("new_k", new_k, dev), _cuda("new_v", new_v, dev),
+            _cuda("slot_mapping", slot_mapping, dev), _dtype_code(new_k), _stream_handle(stream))
     _check("paged_decode_step_shared_prefix", st)
 
 
@@ -967,9 +967,11 @@ def _workspace(workspace, sizes, parts, dev, stream):
 
 
 def _new_workspace(n, old, dev, handle):
-    if old is not None:
-        torch.cuda.synchronize(dev)   # the smaller one may still be in use on its stream
     ws = torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", dev))
+    # the smaller one may still be in use on its stream, and what the current stream has queued may
+    # still use the memory that it gave for a call on another one
+    if torch.cuda.is_initialized() and (old is not None or handle.value != _stream_handle(None).value):
+        torch.cuda.synchronize(dev)
     _check("pkv_workspace_init", load_library().pkv_workspace_init(_cuda("workspace", ws), n, handle))
     return ws
 
