@@ -413,11 +413,32 @@ def paged_attention_decode_head_scales(out, q, k_cache, v_cache, block_tables, s
     _check("paged_attention_decode_head_scales", st)
 
 
-def read_device_error(workspace: torch.Tensor, clear: bool = False, stream=None) -> int:
-    """The workspace's device error word (PKV_DEVERR_* bits); synchronises the stream."""
+def read_device_error(workspace: torch.Tensor | None = None, clear: bool = False, stream=None) -> int:
+    """The workspace's device error word (PKV_DEVERR_* bits); synchronises the stream. Without a workspace:
+    the bits of all that the binding keeps for calls on `stream` of the current device. Cleared after
+    DEVERR_TIMEOUT, a kept workspace is initialised anew, as one of the caller's has to be. (Calls captured
+    without a workspace have one of the graph's own, which is not among them: give those calls one.)"""
+    if workspace is not None:
+        return _error_word(workspace, clear, _stream_handle(stream))
+    dev = torch.cuda.current_device()
+    handle = _raw_stream(stream, dev)
+    bits = 0
+    for kept in ([k for (_, d, st), k in list(_op_ws.items()) if (d, st) == (dev, handle)] +
+                 [k for (d, _, st), k in list(_ws_cache.items()) if (d, st or 0) == (dev, handle)]):
+        with kept.lock:
+            if kept.tensor is None:
+                continue
+            word = _error_word(kept.tensor, clear, ctypes.c_void_p(handle))
+            if clear and word & DEVERR_TIMEOUT:
+                workspace_init(kept.tensor, handle)
+            bits |= word
+    return bits
+
+
+def _error_word(workspace, clear, handle) -> int:
     v = ctypes.c_int32(0)
     _check("pkv_read_device_error", load_library().pkv_read_device_error(
-        _cuda("workspace", workspace), workspace.numel(), ctypes.byref(v), int(clear), _stream_handle(stream)))
+        _cuda("workspace", workspace), workspace.numel(), ctypes.byref(v), int(clear), handle))
     return int(v.value)
 
 
