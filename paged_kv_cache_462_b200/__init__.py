@@ -142,6 +142,8 @@ def _bind_fast(lib) -> None:
         from . import _fastcall
     except ImportError:
         return
+    if getattr(_fastcall, "torch_version", None) != torch.__version__:
+        return
     for name in ("qk_norm_rope", "qk_norm_rope_and_cache", "reshape_and_cache_block_scales",
                  "paged_attention_decode_block_scales", "update_key_bounds", "select_blocks",
                  "paged_attention_decode_sparse", "pkv_stream_recorded"):

@@ -4,13 +4,15 @@
 
 Each .cu file compiles to an object in parallel; the objects link into
 ``paged_kv_cache_462_b200/libpagedkv.so`` (the CUDA runtime linked statically). The binding's
-hot path, ``csrc/fastcall.cpp``, becomes the extension module ``_fastcall.so`` beside it.
+hot path, ``csrc/fastcall.cpp``, becomes the extension module ``_fastcall`` beside it, for the Python and
+torch that build it; the package works without it, only slower, so that a failure there is a warning.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import subprocess
@@ -21,7 +23,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libpagedkv.so")
-FASTCALL = os.path.join(HERE, "_fastcall.so")
+FASTCALL = os.path.join(HERE, "_fastcall" + sysconfig.get_config_var("EXT_SUFFIX"))   # one file a Python
 BUILD_DIR = os.path.join(HERE, "_build")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -56,26 +58,57 @@ def up_to_date() -> bool:
     return _newer(LIB, _deps())
 
 
+def torch_version() -> str:
+    """The installed torch's version ("" without one), as its package metadata has it."""
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return ""
+
+
 def build_fastcall(force: bool = False) -> str:
-    """The extension module _fastcall.so (g++, torch's and Python's headers)."""
+    """The extension module _fastcall (g++, torch's and Python's headers). Rebuilt for another torch: the
+    version it was built for stands in a file beside the objects, and in the module."""
     src = os.path.join(CSRC, "fastcall.cpp")
-    if not force and _newer(FASTCALL, [src, os.path.join(INCLUDE, "pkv.h")]):
-        return FASTCALL
-    torch_dir = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    stamp = os.path.join(BUILD_DIR, os.path.basename(FASTCALL) + ".torch")
+    version = torch_version()
+    spec = importlib.util.find_spec("torch")
+    if not version or spec is None:
+        raise RuntimeError("_fastcall needs torch's headers")
+    if not force and _newer(FASTCALL, [src, os.path.join(INCLUDE, "pkv.h")]) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == version:
+                return FASTCALL
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    torch_dir = list(spec.submodule_search_locations)[0]
     tmp = FASTCALL + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE,
-           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"),
+           f'-DPKV_TORCH_VERSION="{version}"', "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(torch_dir, "include"),
            "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), src,
            "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, FASTCALL)
+    with open(stamp, "w") as f:
+        f.write(version)
     return FASTCALL
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    build_fastcall(force)
+def build(force: bool = False, verbose: bool = False, strict: bool = False) -> str:
+    """The library, then the extension module; `strict` raises where that one cannot be built."""
+    build_library(force, verbose)
+    try:
+        build_fastcall(force)
+    except (OSError, RuntimeError) as e:
+        if strict:
+            raise
+        print(f"warning: built without the binding's hot path: {e}", file=sys.stderr)
+    return LIB
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)

@@ -390,4 +390,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", "Hot path of the bindi
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__fastcall() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__fastcall()
+{
+    PyObject* m = PyModule_Create(&module);
+    // the torch whose at::Tensor this was compiled against: with another one the package leaves it alone
+    if (m && PyModule_AddStringConstant(m, "torch_version", PKV_TORCH_VERSION) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
