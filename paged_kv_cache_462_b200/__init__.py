@@ -369,7 +369,7 @@ def reshape_and_cache(k, v, k_cache, v_cache, slot_mapping, k_scale=1.0, v_scale
         raise ValueError("shape mismatch between rows and caches")
     if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
         raise TypeError("slot_mapping must be int64 [num_tokens]")
-    err = ctypes.c_void_p(None) if device_error is None else _cuda("device_error", device_error, dev)
+    err = ctypes.c_void_p(_error_ptr(device_error, dev))
     st = load_library().reshape_and_cache(
         _cuda("k", k, dev), _cuda("v", v, dev), _cuda("k_cache", k_cache, dev), _cuda("v_cache", v_cache, dev),
         _cuda("slot_mapping", slot_mapping, dev), T, Hkv, D, BS, NB, _dtype_code(k), _dtype_code(k_cache),
@@ -393,7 +393,7 @@ def reshape_and_cache_head_scales(k, v, k_cache, v_cache, slot_mapping, k_head_s
         raise ValueError("shape mismatch between rows and caches")
     if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
         raise TypeError("slot_mapping must be int64 [num_tokens]")
-    err = ctypes.c_void_p(None) if device_error is None else _cuda("device_error", device_error, dev)
+    err = ctypes.c_void_p(_error_ptr(device_error, dev))
     st = load_library().reshape_and_cache_head_scales(
         _cuda("k", k, dev), _cuda("v", v, dev), _cuda("k_cache", k_cache, dev), _cuda("v_cache", v_cache, dev),
         _cuda("slot_mapping", slot_mapping, dev), T, Hkv, D, BS, NB, _dtype_code(k), _dtype_code(k_cache),
@@ -582,8 +582,14 @@ def _ptr(name, t, dev):
     return _cuda(name, t, dev).value
 
 
-def _opt_ptr(name, t, dev):
-    return None if t is None else _ptr(name, t, dev)
+def _error_ptr(t, dev):
+    """Pointer of the int32 word that a call sets its error bits in (None: none): four bytes, aligned."""
+    if t is None:
+        return None
+    at = _ptr("device_error", t, dev)
+    if t.dtype != torch.int32 or t.numel() < 1:
+        raise TypeError("device_error must be an int32 tensor of one element or more")
+    return at
 
 
 def _rows(name, t, dev, heads=None, dim=None, dtype=None):
@@ -648,7 +654,7 @@ def qk_norm_rope(q_out, k_out, q, k, q_weight, k_weight, eps, cos_sin, positions
         ko = _ptr("k_out", k_out, dev)
     _check("qk_norm_rope", load_library().qk_norm_rope(
         qo, ko, qp, kp, qw, kw, float(eps), cs, pos, T, Hq, Hkv, D, R, NP, bool(interleaved), qs, ks, dt,
-        _opt_ptr("device_error", device_error, dev), _raw_stream(stream, dev)))
+        _error_ptr(device_error, dev), _raw_stream(stream, dev)))
 
 
 def qk_norm_rope_and_cache(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, positions, k_cache, v_cache,
@@ -676,7 +682,7 @@ def qk_norm_rope_and_cache(q_out, q, k, v, q_weight, k_weight, eps, cos_sin, pos
         sm = _ptr("slot_mapping", slot_mapping, dev)
     _check("qk_norm_rope_and_cache", load_library().qk_norm_rope_and_cache(
         qo, qp, kp, vp, qw, kw, float(eps), cs, pos, kc, vc, sm, T, Hq, Hkv, D, R, NP, BS, NB, bool(interleaved), qs,
-        ks, vs, dt, kdt, float(k_scale), float(v_scale), _opt_ptr("device_error", device_error, dev),
+        ks, vs, dt, kdt, float(k_scale), float(v_scale), _error_ptr(device_error, dev),
         _raw_stream(stream, dev)))
 
 
@@ -731,7 +737,7 @@ def reshape_and_cache_block_scales(k, v, k_cache, v_cache, k_block_scales, v_blo
         dt, kdt = _dtype_code(k), _dtype_code(k_cache)
     _check("reshape_and_cache_block_scales", load_library().reshape_and_cache_block_scales(
         kp, vp, kc, vc, kbs, vbs, bt, sl, ro, T, S, Hkv, D, BS, MB, NB, ks, vs, dt, kdt,
-        _opt_ptr("device_error", device_error, dev), _raw_stream(stream, dev)))
+        _error_ptr(device_error, dev), _raw_stream(stream, dev)))
 
 
 def _decode_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, dev):
@@ -793,7 +799,7 @@ def update_key_bounds(key_bounds, k_cache, block_tables, seq_lens, row_offsets, 
         kb, kc, kdt = _ptr("key_bounds", key_bounds, dev), _ptr("k_cache", k_cache, dev), _dtype_code(k_cache)
     _check("update_key_bounds", load_library().update_key_bounds(
         kb, kc, bt, sl, ro, int(num_tokens), S, Hkv, D, BS, MB, NB, kdt, float(k_scale), scales or None,
-        _opt_ptr("device_error", device_error, dev), _raw_stream(stream, dev)))
+        _error_ptr(device_error, dev), _raw_stream(stream, dev)))
 
 
 def select_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq) -> int:
