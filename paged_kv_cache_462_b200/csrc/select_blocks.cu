@@ -19,7 +19,9 @@
 // MMAs stay under 35 * 2^-23 of their own |terms|, 2 head_dim / 32 <= 8 additions under 2^-24 A each).
 // Blocks further than that from the border are decided by the fp32 score; those within it are
 // scored again in fp64, where products of bf16 numbers and their sums are exact but for terms
-// 2^-30 apart. A block whose score is not finite ranks first.
+// 2^-30 apart. Products and sums below fp32's normal range lose more than that: 3 head_dim of them by
+// 2^-126 at most each, which every border allows for (2^-115 for two scores). A block whose score is not
+// finite ranks first.
 //
 // Two launches. The first streams the bounds: a block's bounds of neighbouring KV heads are one run of
 // memory, so a producer warp brings 16 blocks (or a few times 16) of up to four heads at a time into
@@ -54,6 +56,7 @@ constexpr int kSelWideThreads = 1024, kSelWidePerThread = 16;
 constexpr int kSelNear = 256;                 // blocks near the border that are ranked in shared memory
 constexpr int kSelSmemKeys = 4096;            // what registers cannot settle is selected in shared memory up to this many
 constexpr float kSelError = 7.62939453125e-06f;   // 2^-17
+constexpr float kSelTiny = 2.407412430484045e-35f; // 2^-115
 constexpr uint32_t kChosen = 0xffffffffu;
 
 struct SelectArgs {
@@ -483,13 +486,14 @@ __device__ __forceinline__ double exact_score(const __nv_bfloat16* q, const __nv
 }
 
 // The keys from `up` on are certainly above a border `key`, those below `down` certainly not: two
-// errors (the border's own and the block's) and the rounding of this very sum.
+// errors (the border's own and the block's), the rounding of this very sum and what is lost below fp32's
+// normal range.
 __device__ __forceinline__ void border_zone(uint32_t key, float mag, uint32_t& down, uint32_t& up)
 {
     const float f = __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
     up = down = key;
     if (finite(f)) {
-        const float d = 2.f * kSelError * mag + fabsf(f) * 2.4e-7f;
+        const float d = 2.f * kSelError * mag + fabsf(f) * 2.4e-7f + kSelTiny;
         up = max(key, sort_key(f + d));
         down = min(key, sort_key(f - d));
     }
