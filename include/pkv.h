@@ -425,6 +425,9 @@ PKV_API int qk_norm_rope_and_cache(void* q_out, const void* q, const void* k, co
  *
  * paged_attention_decode_block_scales is paged_attention_decode over such a cache. Any positive
  * scales can be given, V scales within 2^-50 .. 2^50 (others are taken as the nearest of these).
+ * A token's weight times its V scale enters the products in f16: below 2^-21 of the sequence's
+ * largest it loses bits, below 2^-32 it is left out. So a scale should fit what its block holds, as
+ * the append's do: one far too large takes precision from the other blocks.
  * Shapes as the tensor-core kernel's 8-bit ones (bf16 q, head_dim 128, block_size 16 or 32); q
  * 16-byte aligned. pkv_set_fp8_kernel's choice does not apply.
  */

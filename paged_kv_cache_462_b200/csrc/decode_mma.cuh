@@ -327,8 +327,9 @@ struct MmaCfg {
 // Block scales: value = code * scale with a scale per tile, so a tile's scores are s = ks (q.K) and
 // its output weights are vs p. The accumulators hold 2^(s + log2 vs - m), a number of the size of
 // the tile's share of the output whatever its scale, which keeps f16 weights clear of its
-// subnormals; m is the running maximum of s + log2 vs, and the sum of the weights themselves takes
-// 2^(s + log2 vs - m) / vs. Scales per tensor stay outside (ks = vs = 1).
+// subnormals where scales fit their blocks; m follows the maximum of s + log2 vs, and the sum of the
+// weights themselves takes 2^(s + log2 vs - m) / vs. Scales per tensor stay outside (ks = vs = 1).
+// A weight below 2^-32 of the sequence's largest is zero in f16.
 struct __align__(16) UnitHead {
     int valid;      // tokens of the tile that exist (0: none, or no tile)
     float ks;
@@ -468,8 +469,11 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
     constexpr int W = C::W;
     constexpr bool F16 = C::kF16;
     constexpr bool I8 = C::kI8;
-    // lazy running max: moved only when a tile max passes it by kSlack (log2 units), so p <= 2^8
-    constexpr float kSlack = kMmaRescaleSlack;
+    // lazy running reference: moved only when a tile max passes it by kSlack (log2 units), to kAbove below that
+    // max, so p <= 2^kSlack. PH over 8-bit caches: blocks' V scales spread the weights, and kAbove uses f16's
+    // range to its top (2^15), so that a weight 2^-21 of the largest is still a normal number.
+    constexpr float kAbove = PH && F16 ? 7.0f : 0.0f;
+    constexpr float kSlack = kMmaRescaleSlack + kAbove;
     const int S = p.stages_per_warp;   // ring depth (stages of the CTA)
     const int Hkv = p.num_kv_heads;
     const int NHG = Hkv / HG;          // head groups per sequence
@@ -1106,7 +1110,7 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
                                 bm1 = fmaxf(bm1, __shfl_xor_sync(kFullMask, bm1, off));
                             }
                             const bool up0 = bm0 > m[0] + kSlack, up1 = bm1 > m[1] + kSlack;
-                            const float n0 = up0 ? bm0 : m[0], n1 = up1 ? bm1 : m[1];
+                            const float n0 = up0 ? bm0 - kAbove : m[0], n1 = up1 ? bm1 - kAbove : m[1];
                             const float a0 = up0 ? fast_exp2(m[0] - n0) : 1.f, a1 = up1 ? fast_exp2(m[1] - n1) : 1.f;
                             m[0] = n0;
                             m[1] = n1;
