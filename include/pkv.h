@@ -413,7 +413,8 @@ PKV_API int qk_norm_rope_and_cache(void* q_out, const void* q, const void* k, co
  *                  seq_lens[s] - n .. seq_lens[s] - 1 (seq_lens counts them). Rows behind the last
  *                  sequence's are not read. Entries out of order or range: PKV_DEVERR_ROWS; more
  *                  rows than tokens, or a length beyond the table: PKV_DEVERR_SEQ_LEN; such a
- *                  sequence is skipped.
+ *                  sequence is skipped. Where entries are out of order, blocks of other
+ *                  sequences may be left out as well (never written wrongly).
  *   k, v           as in qk_norm_rope (k_stride, v_stride in elements), in_dtype F32 or BF16
  * A block's scale becomes the smallest power of two 2^e, e in -50 .. 50, with
  * max |x| <= qmax * 2^e (qmax 448 for E4M3, 57344 for E5M2, 127 for INT8) over the finite new rows
@@ -462,9 +463,10 @@ PKV_API int paged_attention_decode_block_scales(void* out, const void* q, const 
  * them, and -1 behind, if the sequence has no more; else its first num_sink_blocks, its last
  * num_recent_blocks, and of the others those with the highest
  *   score(j) = max over the query heads g of h of sum_d max(q[s][g][d] * max_d, q[s][g][d] * min_d),
- * an upper bound of the products of the block's keys with these queries. Ties go to the lowest
- * index; sums that fp32 cannot tell apart are formed again in fp64. A block whose score is not
- * finite ranks first, one with a bad block id (PKV_DEVERR_BLOCK_ID) last. q is bf16. The
+ * an upper bound of the products of the block's keys with these queries (for 8-bit caches, whose
+ * bounds are rounded to the nearest bf16, up to 2^-8 of sum_d |q_d k_d|). Ties go to the lowest
+ * index; sums that fp32 cannot tell apart are formed again in fp64. A block with a bound that is not
+ * finite, or a score beyond fp32, ranks first, one with a bad block id (PKV_DEVERR_BLOCK_ID) last. q is bf16. The
  * workspace (pkv_select_workspace_size bytes) starts zeroed (pkv_workspace_init) and holds the
  * error word; one can serve calls of any sizes it is large enough for, but calls that share one
  * must not overlap on the GPU, nor be issued by two threads at once, even to one stream. Two

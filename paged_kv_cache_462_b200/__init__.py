@@ -820,7 +820,8 @@ def select_blocks(selected, q, key_bounds, block_tables, seq_lens, block_size, n
     """selected[s, h] (int32 [num_seqs, num_kv_heads, num_selected]) = the logical blocks KV head h's
     queries may need most, ascending, -1 behind where the sequence has fewer: the first
     num_sink_blocks, the last num_recent_blocks and the highest scores of the rest, a block's score
-    being the bound that key_bounds sets to its keys' products with the group's queries.
+    being the bound that key_bounds sets to its keys' products with the group's queries (first of
+    all, blocks with bounds that are not finite).
     q bfloat16 [num_seqs, num_heads, head_dim]."""
     m = _match("select", selected, q, key_bounds, block_tables, seq_lens)
     if m is not None:

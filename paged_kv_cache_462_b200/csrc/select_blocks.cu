@@ -3,7 +3,8 @@
 //
 //   score(j) = max over the group's query heads of sum_d max(q_d kmax_d, q_d kmin_d)
 //
-// with kmax, kmin the block's key bounds: no key of block j has a larger product with the query.
+// with kmax, kmin the block's key bounds: no key of block j has a larger product with the query (but for
+// the rounding of an 8-bit cache's bounds to bf16, up to 2^-8 of sum_d |q_d k_d|).
 // Kept are the first num_sink and the last num_recent blocks and the highest scores of the rest,
 // ties to the lowest index, in ascending order.
 //
@@ -20,8 +21,8 @@
 // Blocks further than that from the border are decided by the fp32 score; those within it are
 // scored again in fp64, where products of bf16 numbers and their sums are exact but for terms
 // 2^-30 apart. Products and sums below fp32's normal range lose more than that: 3 head_dim of them by
-// 2^-126 at most each, which every border allows for (2^-115 for two scores). A block whose score is not
-// finite ranks first.
+// 2^-126 at most each, which every border allows for (2^-115 for two scores). A block with a bound that
+// is not finite, or a score beyond fp32, ranks first.
 //
 // Two launches. The first streams the bounds: a block's bounds of neighbouring KV heads are one run of
 // memory, so a producer warp brings 16 blocks (or a few times 16) of up to four heads at a time into

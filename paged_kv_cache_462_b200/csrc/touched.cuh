@@ -6,7 +6,9 @@
 // Items are numbered without a scan: sequence s owns the numbers from row_offsets[s] / block_size +
 // 2 s up to the next sequence's, which are at least n / block_size + 2, and n consecutive positions
 // lie in at most (n - 2) / block_size + 2 blocks. So the host launches num_tokens / block_size +
-// 2 num_seqs items, knowing no length, and the numbers without a block do nothing.
+// 2 num_seqs items, knowing no length, and the numbers without a block do nothing. (Offsets out of order
+// can hide other sequences' numbers from the search below: their blocks are left out, and the
+// call has flagged the offsets.)
 #pragma once
 
 #include "device.cuh"
