@@ -475,10 +475,10 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
     constexpr float kAbove = PH && F16 ? 7.0f : 0.0f;
     constexpr float kSlack = kMmaRescaleSlack + kAbove;
     // bf16 caches: p.V takes bf16 weights. With up to four query columns, columns 4 .. 7 repeat them and carry
-    // what bf16 leaves of their weights, so that these are good to 2^-16 at no MMA more; both halves of an
-    // output meet at the segment's end. (One sequence, 64 selected blocks 14.4 -> 14.9 us; no difference
-    // beyond 0.5 % on 16 to 256 sequences, dense or sparse. With more columns the weights stay good to
-    // 2^-8: a second product instead cost 1 % at 8 KV heads, 5 % at two and 16 % at one.)
+    // what bf16 leaves of their weights, so that these are good to 2^-15 at no MMA more; both halves of an
+    // output meet at the segment's end. (64 selected blocks: one sequence 14.4 us either way, eight 17.5 -> 18.1
+    // us; 16 to 256 sequences, dense or sparse, alike within 0.5 %. With more columns the weights stay good
+    // to 2^-8: a second product instead cost 1 % at 8 KV heads, 5 % at two and 16 % at one.)
     constexpr bool kLow = !F16 && !PFX && G <= 4;
     const int S = p.stages_per_warp;   // ring depth (stages of the CTA)
     const int Hkv = p.num_kv_heads;
@@ -822,7 +822,9 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
     const int t = lane & 3;    // MMA column pair
 
 
-    [[maybe_unused]] const float low = t >= 2 ? -1.f : 0.f;   // columns 4 .. 7 of kLow
+    // kLow: columns 0 .. 3 take a weight's upper part h, columns 4 .. 7 the rest, w - h
+    [[maybe_unused]] const float upper = t < 2 ? 1.f : -1.f;
+    [[maybe_unused]] const uint32_t rest = t < 2 ? 0u : 0xffffffffu;
     int st = 0;                // ring position: the stage, and the parity of its turn
     uint32_t turn = 0;
     for (int ordinal = 0;; ++ordinal) {
@@ -1150,14 +1152,15 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
                         uint32_t pb0, pb1;
                         {
                             // ---- P^T as the B operand: b0 = (tokens 2t, 2t+1; head g), b1 = (tokens 2t+8, 2t+9; head g)
-                            uint32_t X = pack2<F16>(pr[0], pr[2]);   // head 2t:   tokens g, g+8
-                            uint32_t Y = pack2<F16>(pr[1], pr[3]);   // head 2t+1: tokens g, g+8
-                            if constexpr (kLow) {
-                                X = pack2<F16>(fmaf(low, __uint_as_float(X << 16), pr[0]),
-                                               fmaf(low, __uint_as_float(X & 0xffff0000u), pr[2]));
-                                Y = pack2<F16>(fmaf(low, __uint_as_float(Y << 16), pr[1]),
-                                               fmaf(low, __uint_as_float(Y & 0xffff0000u), pr[3]));
+                            if constexpr (kLow) {   // the upper 16 bits, or the rest
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const uint32_t w = __float_as_uint(pr[i]);
+                                    pr[i] = fmaf(upper, __uint_as_float(w & 0xffff0000u), __uint_as_float(w & rest));
+                                }
                             }
+                            const uint32_t X = pack2<F16>(pr[0], pr[2]);   // head 2t:   tokens g, g+8
+                            const uint32_t Y = pack2<F16>(pr[1], pr[3]);   // head 2t+1: tokens g, g+8
                             const uint32_t xa = __shfl_sync(kFullMask, X, srcA), ya = __shfl_sync(kFullMask, Y, srcA);
                             const uint32_t xb = __shfl_sync(kFullMask, X, srcB), yb = __shfl_sync(kFullMask, Y, srcB);
                             const uint32_t va = (g & 1) ? ya : xa, vb = (g & 1) ? yb : xb;
@@ -1240,14 +1243,19 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
                 l[0] += __shfl_xor_sync(kFullMask, l[0], off);
                 l[1] += __shfl_xor_sync(kFullMask, l[1], off);
             }
+            // this lane's outputs: columns col, col + 1 of tiles dt0 .. dt0 + kOut - 1 of head_dim. kLow: lanes t and
+            // t + 2 hold the two parts of the same columns, and each takes the sums of half the tiles.
+            constexpr int kOut = kLow ? C::kDT / 2 : C::kDT;
+            const int col = kLow ? 2 * (t & 1) : 2 * t, dt0 = kLow ? (t >> 1) * kOut : 0;
             if constexpr (kLow) {
 #pragma unroll
-                for (int dt = 0; dt < C::kDT; ++dt)
+                for (int dt = 0; dt < kOut; ++dt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        // (an infinite V makes the upper part infinite, and the lower one what its sign does)
-                        const float rest = __shfl_xor_sync(kFullMask, o[dt][i], 2);
-                        o[dt][i] += fabsf(o[dt][i]) <= 3.402823466e38f ? rest : 0.f;
+                        const float other = __shfl_xor_sync(kFullMask, t < 2 ? o[dt + kOut][i] : o[dt][i], 2);
+                        const float mine = t < 2 ? o[dt][i] : o[dt + kOut][i], sum = mine + other;
+                        // (an infinite V makes the upper part infinite, and the rest what a zero makes of it)
+                        o[dt][i] = fabsf(sum) <= 3.402823466e38f ? sum : t < 2 ? mine : other;
                     }
             }
             const int first_run = ch.of(stream_begin);   // chunks holding pieces of this stream
@@ -1255,7 +1263,7 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
             const int stream = s * NHG + hg;
             // element (head column c, row d) of this lane's accumulators
             auto d_of = [&](int dt, int half) -> int {
-                return dt * 16 + g + 8 * half;
+                return (dt0 + dt) * 16 + g + 8 * half;
             };
             // a whole stream writes `out`; pieces of split streams, every stream of a prefix pass and
             // the suffix of a sequence with shared blocks leave (o, m, l) for the merge
@@ -1265,26 +1273,26 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
                 const float inv0 = l[0] > 0.f ? out_scale / l[0] : 0.f;
                 const float inv1 = l[1] > 0.f ? out_scale / l[1] : 0.f;
 #pragma unroll
-                for (int dt = 0; dt < C::kDT; ++dt)
+                for (int dt = 0; dt < kOut; ++dt)
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int d = d_of(dt, half);
-                        if (2 * t < G)
+                        if (col < G)
                             from_float(o[dt][2 * half] * inv0, out0 + d);
-                        if (2 * t + 1 < G)
+                        if (col + 1 < G)
                             from_float(o[dt][2 * half + 1] * inv1, out1 + d);
                     }
             } else {
                 float* part = p.partials + ((size_t)(cur + stream) * W + warp) * p.slot_floats;
 #pragma unroll
-                for (int dt = 0; dt < C::kDT; ++dt)
+                for (int dt = 0; dt < kOut; ++dt)
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int d = d_of(dt, half);
-                        if (2 * t < G)
-                            part[(2 * t) * D + d] = o[dt][2 * half];
-                        if (2 * t + 1 < G)
-                            part[(2 * t + 1) * D + d] = o[dt][2 * half + 1];
+                        if (col < G)
+                            part[col * D + d] = o[dt][2 * half];
+                        if (col + 1 < G)
+                            part[(col + 1) * D + d] = o[dt][2 * half + 1];
                     }
                 if (g == 0) {
                     if (2 * t < G) {
