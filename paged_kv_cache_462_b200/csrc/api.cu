@@ -463,7 +463,7 @@ int heads_impl(void* out, const void* q, const void* k_cache, const void* v_cach
             runs = 16 * streams > sms * kMaxRunsPerSM ? (int)(16 * streams) : sms * kMaxRunsPerSM;
         // Few units: four to a run, not one. A run's copies are in flight together, so more units cost it
         // little, while every run leaves a piece of each stream to merge (one sequence, 64 selected
-        // blocks: 16.4 us with 32 runs, 21.5 us with 296).
+        // blocks: 14.4 us with 32 runs, 21.3 us with 296).
         const long long width = selected && num_selected < max_blocks_per_seq ? num_selected : max_blocks_per_seq;
         const long long units = (long long)num_seqs * (num_kv_heads / HG) * width;
         if (units > 0 && runs > (units + 3) / 4) {
@@ -485,8 +485,8 @@ int heads_impl(void* out, const void* q, const void* k_cache, const void* v_cach
     p.sel_width = num_selected;
     p.k_block_scales = k_block_scales;
     p.v_block_scales = v_block_scales;
-    // (a grid of few runs ends as one: waiting for it beats polling its stamps: 15.7 us to the 16.4 us
-    // above, and 16.4 to 18.5 us for eight sequences)
+    // (a grid of few runs ends as one: waiting for it beats polling its stamps: 14.4 to 15.6 us for the one
+    // sequence above, 18.1 to 18.5 us for eight)
     // (and the workspace has stamps for `sized` runs)
     if (few || sized < runs || recorded(static_cast<cudaStream_t>(stream)))
         p.chunk_done = nullptr;

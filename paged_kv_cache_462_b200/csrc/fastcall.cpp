@@ -33,7 +33,7 @@ namespace {
 //   name : sizes : layout : type
 // sizes: symbols (bound where they first appear), numbers, or symbol+number; layout `c` contiguous or
 // `rows` ([tokens, heads, dim], a token's heads contiguous, tokens apart); type i (int32), l (int64),
-// f (float32), b (bfloat16), u (uint8), X (float32 or bfloat16, the same for every X), K (a cache's
+// f (float32), b (bfloat16), X (float32 or bfloat16, the same for every X), K (a cache's
 // type, the same for every K). A leading `?` takes None for a null pointer.
 struct Size {
     int symbol;     // -1: a number
@@ -174,7 +174,6 @@ PyObject* match_or_throw(PyObject* const* args, Py_ssize_t n)
         case 'l': ok = type == at::ScalarType::Long; break;
         case 'f': ok = type == at::ScalarType::Float; break;
         case 'b': ok = type == at::ScalarType::BFloat16; break;
-        case 'u': ok = type == at::ScalarType::Byte; break;
         case 'X':
             if (x_type == at::ScalarType::Undefined) {
                 x_type = type;

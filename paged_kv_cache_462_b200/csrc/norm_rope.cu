@@ -8,7 +8,8 @@
 // Everything is fp32 from the load to the one rounding of each stored element; the sum of
 // squares is fp32 too. Bound: HBM (each row is read once and written once), with the issue slots not
 // far behind. Measured (40 query and 8 KV heads of 128, bf16, 8192 tokens, 239 MB): 44.8 us, 5.3 TB/s,
-// 82 % of the copy rate; with a CTA per token and a load per row 63 us, 70 % of the issue slots busy.
+// 82 % of the copy rate, where a call finds what the one before left in L2, 49.1 us, 75 %, with other
+// inputs each time; with a CTA per token and a load per row 63 us, 70 % of the issue slots busy.
 // Four tokens: 3.5 us, launch and latency.
 //
 // Layout: a row is held by head_dim / 8 lanes (16 or 8), 8 elements each, as two chunks of four
