@@ -698,6 +698,7 @@ __global__ void __launch_bounds__(MmaCfg<KV, D, BS, G, HG, PFX, PH>::kThreads,
                         if (aborted)
                             break;
                         const unsigned live = __ballot_sync(kFullMask, row >= 0);
+                        __syncwarp();   // lane 0's wait, before other lanes write what consumers have read
                         if (lane < HG) {
                             vs = fminf(fmaxf(vs, kBlockScaleLo), kBlockScaleHi);
                             UnitHead u;

@@ -323,6 +323,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_blocks_kernel(const Se
             aborted = __shfl_sync(kFullMask, aborted ? 1 : 0, 0) != 0;
             if (aborted)
                 break;
+            __syncwarp();                // lane 0's wait, before other lanes write what consumers have read
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (lane + 32 * i < stage_blocks)
