@@ -22,6 +22,7 @@ Entry points (same names as the C ABI):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -265,7 +266,10 @@ def paged_attention_decode(out, q, k_cache, v_cache, block_tables, seq_lens, sca
     """
     args, sizes, dev = _decode_args(out, q, k_cache, v_cache, block_tables, seq_lens, scale, k_scale, v_scale,
                                     num_partitions)
-    with _workspace(workspace, sizes, num_partitions, dev, stream) as ws:
+    n = 0 if workspace is not None else workspace_size(*sizes, num_partitions)
+    use = _workspace(workspace, n, num_partitions, dev, stream)
+    with use.lock:
+        ws = use.ready(n)
         st = load_library().paged_attention_decode(*args, _cuda("workspace", ws, dev), ws.numel(),
                                                    _stream_handle(stream))
     _check("paged_attention_decode", st)
@@ -308,7 +312,10 @@ def paged_attention_decode_mq(out, q, k_cache, v_cache, block_tables, seq_lens, 
         raise TypeError("block_tables and seq_lens must be int32")
     if block_tables.dim() != 2 or block_tables.shape[0] != S or seq_lens.shape != (S,):
         raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
-    with _workspace(workspace, (S, Hq * QL, Hkv, D), num_partitions, dev, stream) as ws:
+    n = 0 if workspace is not None else workspace_size(S, Hq * QL, Hkv, D, num_partitions)
+    use = _workspace(workspace, n, num_partitions, dev, stream)
+    with use.lock:
+        ws = use.ready(n)
         st = load_library().paged_attention_decode_mq(
             _cuda("out", out, dev), _cuda("q", q, dev), _cuda("k_cache", k_cache, dev),
             _cuda("v_cache", v_cache, dev), _cuda("block_tables", block_tables, dev),
@@ -348,7 +355,10 @@ def paged_decode_step(out, q, k_cache, v_cache, block_tables, seq_lens, new_k, n
         raise TypeError("block_tables and seq_lens must be int32")
     if block_tables.dim() != 2 or block_tables.shape[0] != S or seq_lens.shape != (S,):
         raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
-    with _workspace(workspace, (S, Hq, Hkv, D), num_partitions, dev, stream) as ws:
+    n = 0 if workspace is not None else workspace_size(S, Hq, Hkv, D, num_partitions)
+    use = _workspace(workspace, n, num_partitions, dev, stream)
+    with use.lock:
+        ws = use.ready(n)
         st = load_library().paged_decode_step(
             _cuda("out", out, dev), _cuda("q", q, dev), _cuda("k_cache", k_cache, dev),
             _cuda("v_cache", v_cache, dev), _cuda("block_tables", block_tables, dev),
@@ -409,7 +419,10 @@ def paged_attention_decode_head_scales(out, q, k_cache, v_cache, block_tables, s
     Hkv = k_cache.shape[1]
     args = (*args[:16], _head_scales("k_head_scales", k_head_scales, Hkv, dev),
             _head_scales("v_head_scales", v_head_scales, Hkv, dev), *args[18:])
-    with _workspace(workspace, sizes, num_partitions, dev, stream) as ws:
+    n = 0 if workspace is not None else workspace_size(*sizes, num_partitions)
+    use = _workspace(workspace, n, num_partitions, dev, stream)
+    with use.lock:
+        ws = use.ready(n)
         st = load_library().paged_attention_decode_head_scales(*args, _cuda("workspace", ws, dev), ws.numel(),
                                                                _stream_handle(stream))
     _check("paged_attention_decode_head_scales", st)
@@ -492,7 +505,7 @@ def _plan_args(plan: DevicePrefixPlan, dev, S, MB):
 
 def _shared_prefix_workspace(workspace, S, Hq, Hkv, D, plan, num_partitions, dev, stream):
     n = 0 if workspace is not None else shared_prefix_workspace_size(S, Hq, Hkv, D, plan.num_groups, num_partitions)
-    return _op_workspace(workspace, "shared_prefix", n, dev, _raw_stream(stream, dev))
+    return _op_workspace(workspace, "shared_prefix", n, dev, _raw_stream(stream, dev)), n
 
 
 def paged_attention_decode_shared_prefix(out, q, k_cache, v_cache, block_tables, seq_lens, plan, scale,
@@ -508,7 +521,9 @@ def paged_attention_decode_shared_prefix(out, q, k_cache, v_cache, block_tables,
     if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32 or block_tables.dim() != 2 \
             or block_tables.shape[0] != S or seq_lens.shape != (S,):
         raise ValueError("block_tables must be int32 [num_seqs, max_blocks] and seq_lens int32 [num_seqs]")
-    with _shared_prefix_workspace(workspace, S, Hq, Hkv, D, plan, num_partitions, dev, stream) as ws:
+    use, n = _shared_prefix_workspace(workspace, S, Hq, Hkv, D, plan, num_partitions, dev, stream)
+    with use.lock:
+        ws = use.ready(n)
         st = load_library().paged_attention_decode_shared_prefix(
             _cuda("out", out, dev), _cuda("q", q, dev), _cuda("k_cache", k_cache, dev),
             _cuda("v_cache", v_cache, dev), _cuda("block_tables", block_tables, dev),
@@ -535,7 +550,9 @@ def paged_decode_step_shared_prefix(out, q, k_cache, v_cache, block_tables, seq_
         raise ValueError("new_k/new_v must be [num_seqs, num_kv_heads, head_dim] of one dtype")
     if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (S,):
         raise TypeError("slot_mapping must be int64 [num_seqs]")
-    with _shared_prefix_workspace(workspace, S, Hq, Hkv, D, plan, num_partitions, dev, stream) as ws:
+    use, n = _shared_prefix_workspace(workspace, S, Hq, Hkv, D, plan, num_partitions, dev, stream)
+    with use.lock:
+        ws = use.ready(n)
         st = load_library().paged_decode_step_shared_prefix(
             _cuda("out", out, dev), _cuda("q", q, dev), _cuda("k_cache", k_cache, dev),
             _cuda("v_cache", v_cache, dev), _cuda("block_tables", block_tables, dev),
@@ -773,7 +790,9 @@ def paged_attention_decode_block_scales(out, q, k_cache, v_cache, block_tables, 
         dt, kdt = _dtype_code(q), _dtype_code(k_cache)
     st = _raw_stream(stream, dev)
     n = 0 if workspace is not None else _sized(workspace_size, dev, S, Hq, Hkv, D, num_partitions)
-    with _op_workspace(workspace, "decode", n, dev, st) as ws:
+    use = _op_workspace(workspace, "decode", n, dev, st)
+    with use.lock:
+        ws = use.ready(n)
         _check("paged_attention_decode_block_scales", load_library().paged_attention_decode_block_scales(
             op, qp, kp, vp, bt, sl, S, Hq, Hkv, D, BS, float(scale), MB, NB, dt, kdt, ks, vs, int(num_partitions),
             _ptr("workspace", ws, dev), ws.numel(), st))
@@ -841,7 +860,9 @@ def select_blocks(selected, q, key_bounds, block_tables, seq_lens, block_size, n
         sel, qp, kb = _ptr("selected", selected, dev), _ptr("q", q, dev), _ptr("key_bounds", key_bounds, dev)
     st = _raw_stream(stream, dev)
     n = 0 if workspace is not None else _sized(select_workspace_size, dev, S, Hkv, max(1, MB))
-    with _op_workspace(workspace, "select", n, dev, st) as ws:
+    use = _op_workspace(workspace, "select", n, dev, st)
+    with use.lock:
+        ws = use.ready(n)
         _check("select_blocks", load_library().select_blocks(
             sel, qp, kb, bt, sl, S, Hq, Hkv, D, int(block_size), MB, NB, W, int(num_sink_blocks),
             int(num_recent_blocks), _ptr("workspace", ws, dev), ws.numel(), st))
@@ -878,7 +899,9 @@ def paged_attention_decode_sparse(out, q, k_cache, v_cache, block_tables, seq_le
         sel, dt, kdt = _ptr("selected", selected, dev), _dtype_code(q), _dtype_code(k_cache)
     st = _raw_stream(stream, dev)
     n = 0 if workspace is not None else _sized(workspace_size, dev, S, Hq, Hkv, D, num_partitions)
-    with _op_workspace(workspace, "decode", n, dev, st) as ws:
+    use = _op_workspace(workspace, "decode", n, dev, st)
+    with use.lock:
+        ws = use.ready(n)
         _check("paged_attention_decode_sparse", load_library().paged_attention_decode_sparse(
             op, qp, kp, vp, bt, sl, sel, S, Hq, Hkv, D, BS, float(scale), MB, NB, W, dt, kdt, float(k_scale),
             float(v_scale), ks or None, vs or None, int(num_partitions), _ptr("workspace", ws, dev), ws.numel(), st))
@@ -901,47 +924,36 @@ class _Kept:
     """A workspace that the binding keeps for one stream, and its lock: a call holds it from the choice of the
     workspace until its launches are queued. They are two that hand over through the workspace, and the
     C call lets other threads run: their launches on the same stream would go in between."""
-    __slots__ = ("tensor", "lock")
+    __slots__ = ("tensor", "lock", "new", "args")
 
-    def __init__(self):
+    def __init__(self, new, *args):
         self.tensor = None
         self.lock = threading.RLock()
+        self.new, self.args = new, args
 
-    def __enter__(self):
+    def ready(self, n):
+        """The workspace, of n bytes at least (the lock is held)."""
+        if self.tensor is None or self.tensor.numel() < n:
+            self.tensor = self.new(n, self.tensor, *self.args)
         return self.tensor
-
-    def __exit__(self, *_):
-        self.lock.release()
 
 
 class _Given:
     """A workspace that one call alone uses, or that its caller answers for."""
     __slots__ = ("tensor",)
+    lock = contextlib.nullcontext()
 
     def __init__(self, tensor):
         self.tensor = tensor
 
-    def __enter__(self):
+    def ready(self, n):
         return self.tensor
 
-    def __exit__(self, *_):
-        pass
 
-
-def _hold(table, key, n, new, *args) -> _Kept:
-    """The workspace of at least n bytes that `table` keeps under `key`, its lock taken (``with`` gives the
-    tensor and frees the lock); new(n, old, *args) makes one."""
+def _kept(table, key, new, *args) -> _Kept:
+    """What `table` keeps under `key`; new(n, old, *args) makes its workspaces."""
     kept = table.get(key)
-    if kept is None:
-        kept = table.setdefault(key, _Kept())
-    kept.lock.acquire()
-    try:
-        if kept.tensor is None or kept.tensor.numel() < n:
-            kept.tensor = new(n, kept.tensor, *args)
-    except BaseException:
-        kept.lock.release()
-        raise
-    return kept
+    return kept if kept is not None else table.setdefault(key, _Kept(new, *args))
 
 
 def _recorded(stream, current) -> bool:
@@ -969,7 +981,7 @@ def _op_workspace(workspace, kind, n, dev, stream):
         return _Given(workspace)
     if _recorded(stream, _current_raw_stream(dev)):
         return _Given(_new_op_workspace(n, None, dev, stream))
-    return _hold(_op_ws, (kind, dev, stream), n, _new_op_workspace, dev, stream)
+    return _kept(_op_ws, (kind, dev, stream), _new_op_workspace, dev, stream)
 
 
 def _new_op_workspace(n, _, dev, stream):
@@ -984,16 +996,16 @@ def _new_op_workspace(n, _, dev, stream):
 _ws_cache: dict = {}
 
 
-def _workspace(workspace, sizes, parts, dev, stream):
+def _workspace(workspace, n, parts, dev, stream):
     """The caller's workspace, or one kept per (device, partitions, stream), so calls on different streams
     never share one; a new one is zeroed by the library on the stream that will use it. While that
     stream is being captured every call gets its own, as in _op_workspace."""
     if workspace is not None:
         return _Given(workspace)
-    handle, n = _stream_handle(stream), workspace_size(*sizes, parts)
+    handle = _stream_handle(stream)
     if _recorded(handle.value or 0, torch.cuda.current_stream().cuda_stream):
         return _Given(_new_op_workspace(n, None, dev, handle.value or 0))
-    return _hold(_ws_cache, (dev, parts, handle.value), n, _new_workspace, dev, handle)
+    return _kept(_ws_cache, (dev, parts, handle.value), _new_workspace, dev, handle)
 
 
 def _new_workspace(n, old, dev, handle):

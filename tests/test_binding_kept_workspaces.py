@@ -104,3 +104,21 @@ def test_shared_prefix_on_a_stream_given_by_argument():
         pkv.paged_attention_decode_shared_prefix(out, g.q, g.kc, g.vc, g.bt, g.sl, dplan, float(b.scale), stream=stream)
         torch.cuda.synchronize()
         assert max_err(out, ref) <= TOL["bf16"]
+
+
+@pytest.mark.parametrize("where", ["pkv_workspace_init", "paged_attention_decode_sparse"])
+def test_an_interrupted_call_frees_the_workspace(order, monkeypatch, where):
+    """Ctrl-C in the library's calls: another thread can use the workspace after it."""
+    from test_binding_threads import calls
+    real = type(order).__getattr__
+
+    def interrupted(self, name):
+        def stop(*a):
+            raise KeyboardInterrupt
+        return stop if name == where else real(self, name)
+    with monkeypatch.context() as m:
+        m.setattr(type(order), "__getattr__", interrupted)
+        with pytest.raises(KeyboardInterrupt):
+            calls()["sparse"]()
+    run_threads([calls()["sparse"]] * 2, 2)
+    assert len([c for c in order.calls if c[0] == "paged_attention_decode_sparse"]) == 4
